@@ -42,6 +42,15 @@ mlra_status check_tc_coverage(const mlra_dims* d) {
     return MLRA_OK;
 }
 
+// Shapes the 8-bit cache's decode kernel implements: the tensor-core
+// kernel's, with tiles of 16 heads whatever the branch width.
+mlra_status check_fp8_coverage(const mlra_dims* d) {
+    if (!is_pow2_in(d->page_size, 16, 128)) return MLRA_ERR_UNSUPPORTED;
+    if (!decode_tc_supported(d->branches, d->d_c, d->d_r, d->heads)) return MLRA_ERR_UNSUPPORTED;
+    if ((int64_t)d->batch * ceil_div(d->heads, 16) > kMaxBatch) return MLRA_ERR_UNSUPPORTED;
+    return MLRA_OK;
+}
+
 // Shapes the CUDA-core decode kernel implements (its shared memory holds the
 // whole query block and a 32-token tile).
 mlra_status check_simt_coverage(const mlra_dims* d) {
@@ -84,7 +93,15 @@ const void* device_address(const void* p) {
 }
 
 
-enum class Impl { kTensorCore, kSimt };
+// RoPE pair i turns by turns[i] * p full turns at position p (i < 32).
+void rope_turns(float rope_base, int d_r, double* turns) {
+    for (int i = 0; i < 32; ++i)
+        turns[i] = 2 * i < d_r ? std::pow((double)rope_base, -2.0 * i / d_r) / (2.0 * 3.14159265358979323846) : 0.0;
+}
+
+bool aligned4_or_null(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+enum class Impl { kTensorCore, kSimt, kFp8 };
 
 // Host validation of a decode call and the kernel arguments it implies.
 mlra_status decode_args(Impl impl, const mlra_dims* dims, const void* q_lat, const void* q_rope,
@@ -94,7 +111,9 @@ mlra_status decode_args(Impl impl, const mlra_dims* dims, const void* q_lat, con
                         DecodeArgs* a_out) {
     mlra_status s = check_dims(dims);
     if (s != MLRA_OK) return s;
-    s = impl == Impl::kTensorCore ? check_tc_coverage(dims) : check_simt_coverage(dims);
+    s = impl == Impl::kTensorCore ? check_tc_coverage(dims)
+        : impl == Impl::kSimt     ? check_simt_coverage(dims)
+                                  : check_fp8_coverage(dims);
     if (s != MLRA_OK) return s;
     if (!aligned16(q_lat) || !aligned16(q_rope) || !aligned16(latent_cache) ||
         !aligned16(rope_cache) || !aligned16(block_table) || !aligned16(seqlens) ||
@@ -409,11 +428,100 @@ mlra_status mlra_prepare(const mlra_dims* dims, int32_t d_h, const void* q_c, co
     a.page_size = dims->page_size;
     a.max_pages = dims->max_pages_per_seq;
     a.num_pages = dims->num_pages;
-    for (int i = 0; i < 32; ++i)
-        a.rope_turns[i] = 2 * i < dims->d_r
-                              ? std::pow((double)rope_base, -2.0 * i / dims->d_r) / (2.0 * 3.14159265358979323846)
-                              : 0.0;
+    rope_turns(rope_base, dims->d_r, a.rope_turns);
     return cuda_status(launch_prepare(a, static_cast<cudaStream_t>(stream)));
+}
+
+mlra_status mlra_append_fp8(const mlra_dims* dims, int32_t tokens, const void* c_new, const void* kr_new,
+                            const int32_t* cu_seqlens, const int32_t* seqlens, const int32_t* block_table,
+                            float rope_base, void* latent_cache, void* latent_scale, void* rope_cache,
+                            int32_t* device_status, void* stream) {
+    const mlra_status s = check_dims(dims);
+    if (s != MLRA_OK) return s;
+    if (tokens < 0) return MLRA_ERR_INVALID_ARG;
+    if (dims->d_c < 64 || !is_pow2_in(dims->d_c, 64, 512) || dims->branches > 8 || dims->d_r % 2 != 0 ||
+        dims->d_r > 64 || dims->page_size % kFp8Block != 0)
+        return MLRA_ERR_UNSUPPORTED;
+    if (tokens > 0 && (!aligned16(c_new) || !aligned16(kr_new))) return MLRA_ERR_INVALID_ARG;
+    if (!aligned16(cu_seqlens) || !aligned16(seqlens) || !aligned16(block_table) || !aligned16(latent_cache) ||
+        !aligned16(latent_scale) || !aligned16(rope_cache))
+        return MLRA_ERR_INVALID_ARG;
+    if (!aligned4_or_null(device_status)) return MLRA_ERR_INVALID_ARG;
+    if (!(rope_base > 1.f) || !(rope_base < 3.0e38f)) return MLRA_ERR_INVALID_ARG;
+    AppendFp8Args a;
+    a.c_new = static_cast<const __nv_bfloat16*>(c_new);
+    a.kr_new = static_cast<const __nv_bfloat16*>(kr_new);
+    a.cu_seqlens = cu_seqlens;
+    a.seqlens = seqlens;
+    a.block_table = block_table;
+    a.latent_cache = static_cast<uint8_t*>(latent_cache);
+    a.latent_scale = static_cast<float*>(latent_scale);
+    a.rope_cache = static_cast<__nv_bfloat16*>(rope_cache);
+    a.status = device_status;
+    a.tokens = tokens;
+    a.batch = dims->batch;
+    a.branches = dims->branches;
+    a.d_c = dims->d_c;
+    a.d_r = dims->d_r;
+    a.page_size = dims->page_size;
+    a.max_pages = dims->max_pages_per_seq;
+    a.num_pages = dims->num_pages;
+    a.places = tokens / kFp8Block + 2ll * dims->batch;
+    rope_turns(rope_base, dims->d_r, a.rope_turns);
+    return cuda_status(launch_append_fp8(a, static_cast<cudaStream_t>(stream)));
+}
+
+mlra_status mlra_decode_fp8(const mlra_dims* dims, const void* q_lat, const void* q_rope,
+                            const void* latent_cache, const void* latent_scale, const void* rope_cache,
+                            const int32_t* block_table, const int32_t* seqlens, float scale, float out_scale,
+                            void* out, void* workspace, size_t workspace_bytes, void* stream) {
+    if (dims != nullptr && !aligned16(latent_scale)) return MLRA_ERR_INVALID_ARG;
+    DecodeArgs a;
+    const mlra_status s = decode_args(Impl::kFp8, dims, q_lat, q_rope, latent_cache, rope_cache, block_table,
+                                      seqlens, scale, out_scale, out, workspace, workspace_bytes, &a);
+    if (s != MLRA_OK) return s;
+    return cuda_status(
+        launch_decode_fp8(a, static_cast<const float*>(latent_scale), static_cast<cudaStream_t>(stream)));
+}
+
+mlra_status mlra_prefill(const mlra_dims* dims, int32_t tokens, const void* q_lat, const void* q_rope,
+                         const void* latent_cache, const void* rope_cache, const int32_t* block_table,
+                         const int32_t* seqlens, const int32_t* cu_seqlens, float scale, float out_scale, void* out,
+                         int32_t* device_status, void* stream) {
+    const mlra_status s = check_dims(dims);
+    if (s != MLRA_OK) return s;
+    if (tokens < 0 || (int64_t)tokens * dims->heads > INT32_MAX) return MLRA_ERR_INVALID_ARG;
+    if (!is_pow2_in(dims->page_size, 16, 128) ||
+        !decode_tc_supported(dims->branches, dims->d_c, dims->d_r, dims->heads))
+        return MLRA_ERR_UNSUPPORTED;
+    if (tokens > 0 && (!aligned16(q_lat) || !aligned16(q_rope) || !aligned16(out))) return MLRA_ERR_INVALID_ARG;
+    if (!aligned16(latent_cache) || !aligned16(rope_cache) || !aligned16(block_table) || !aligned16(seqlens) ||
+        !aligned16(cu_seqlens))
+        return MLRA_ERR_INVALID_ARG;
+    if (!aligned4_or_null(device_status)) return MLRA_ERR_INVALID_ARG;
+    if (!(scale == scale) || !(out_scale == out_scale)) return MLRA_ERR_INVALID_ARG;  // NaN
+    PrefillArgs a;
+    a.q_lat = static_cast<const __nv_bfloat16*>(q_lat);
+    a.q_rope = static_cast<const __nv_bfloat16*>(q_rope);
+    a.latent = static_cast<const __nv_bfloat16*>(latent_cache);
+    a.rope = static_cast<const __nv_bfloat16*>(rope_cache);
+    a.block_table = block_table;
+    a.seqlens = seqlens;
+    a.cu_seqlens = cu_seqlens;
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.status = device_status;
+    a.tokens = tokens;
+    a.batch = dims->batch;
+    a.heads = dims->heads;
+    a.branches = dims->branches;
+    a.d_c = dims->d_c;
+    a.d_r = dims->d_r;
+    a.page_size = dims->page_size;
+    a.max_pages = dims->max_pages_per_seq;
+    a.num_pages = dims->num_pages;
+    a.scale_log2 = scale * kLog2e;
+    a.out_scale = out_scale;
+    return cuda_status(launch_prefill(a, static_cast<cudaStream_t>(stream)));
 }
 
 mlra_status mlra_read_device_error(void* workspace, void* stream) {

@@ -145,6 +145,51 @@ struct PrepareArgs {
 cudaError_t launch_prepare(const PrepareArgs& a, cudaStream_t stream);
 size_t prepare_smem_bytes(int d_h);
 
+// ---------------------------------------------------------------------------
+// The 8-bit cache: e4m3 latents with one fp32 scale for every kFp8Block tokens
+// of a page and branch, scale [pages * P / kFp8Block][B].  The append writes
+// powers of two, none below 2^kFp8MinScaleExp (a block of zeros has that one).
+constexpr int kFp8Block = 16;
+constexpr int kFp8MinScaleExp = -40;
+
+// Arguments of the append of token runs to the 8-bit cache (validated on the
+// host).
+struct AppendFp8Args {
+    const __nv_bfloat16* c_new;   // [T, B, d_c]
+    const __nv_bfloat16* kr_new;  // [T, d_r] unrotated
+    const int32_t* cu_seqlens;    // [N + 1] first row of each sequence's run
+    const int32_t* seqlens;       // [N] lengths including the runs
+    const int32_t* block_table;   // [N, max_pages]
+    uint8_t* latent_cache;        // e4m3 [pages, P, B, d_c]
+    float* latent_scale;          // [pages, P / 16, B]
+    __nv_bfloat16* rope_cache;    // [pages, P, d_r]
+    int* status;                  // optional device error word
+    int tokens, batch, branches, d_c, d_r, page_size, max_pages, num_pages;
+    long long places;             // 16-token blocks the grid has room for
+    double rope_turns[32];        // as PrepareArgs
+};
+cudaError_t launch_append_fp8(const AppendFp8Args& a, cudaStream_t stream);
+
+// Split-KV decode over the 8-bit cache (DecodeArgs with the latents as e4m3
+// bytes in `latent` and their scales); see decode_fp8.cu.
+cudaError_t launch_decode_fp8(const DecodeArgs& a, const float* latent_scale, cudaStream_t stream);
+
+// Arguments of the prompt attention (validated on the host).
+struct PrefillArgs {
+    const __nv_bfloat16* q_lat;   // [T, H, B, d_c]
+    const __nv_bfloat16* q_rope;  // [T, H, d_r]
+    const __nv_bfloat16* latent;  // [pages, P, B, d_c]
+    const __nv_bfloat16* rope;    // [pages, P, d_r]
+    const int32_t* block_table;   // [N, max_pages]
+    const int32_t* seqlens;       // [N] lengths including the new tokens
+    const int32_t* cu_seqlens;    // [N + 1] first query row of each sequence
+    __nv_bfloat16* out;           // [T, H, B, d_c]
+    int* status;                  // optional device error word
+    int tokens, batch, heads, branches, d_c, d_r, page_size, max_pages, num_pages;
+    float scale_log2, out_scale;
+};
+cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
+
 // Writes the work partition (see mlra_decode_plan in mlra.h).
 cudaError_t launch_plan_dump(int batch, int page_size, int max_pages, const int32_t* seqlens,
                              int num_ctas, int32_t* plan_out, cudaStream_t stream);

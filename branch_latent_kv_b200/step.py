@@ -4,7 +4,7 @@ A serving loop calls the same decode step every token with the same buffer
 shapes.  ``DecodeStep`` validates the arguments once (one eager call of
 ``mlra_decode`` or, when ``w_uv`` is given, ``mlra_decode_up_proj``: the
 whole step in one launch; batches above 64 use ``mlra_decode`` and
-``mlra_up_proj``), then captures
+``mlra_up_proj``, an 8-bit cache ``mlra_decode_fp8`` and ``mlra_up_proj``), then captures
 the step -- optionally with the host-to-device transfer of its inputs and the
 device-to-host transfer of its result -- into a CUDA graph, so each step costs
 one graph launch on the host.  The inputs cross PCIe in one launch of
@@ -40,13 +40,15 @@ class DecodeStep:
         device tensors): each step copies them to the device first.
     host_output: optional pinned CPU tensor shaped like the step's result
         (``y`` with ``w_uv``, else ``out``): each step copies the result there.
+    latent_scale: the scales of an 8-bit ``latent_cache`` (float8_e4m3fn): the
+        step is then mlra_decode_fp8, followed by mlra_up_proj.
     Calling the step replays the graph on the current stream and returns the
     result tensor (the host one when ``host_output`` is given); synchronise
     before reading host memory.
     """
 
     def __init__(self, q_lat, q_rope, latent_cache, rope_cache, block_table, seqlens, scale,
-                 out_scale, *, w_uv=None, d_h: Optional[int] = None, workspace=None,
+                 out_scale, *, latent_scale=None, w_uv=None, d_h: Optional[int] = None, workspace=None,
                  host_inputs: Optional[Dict[str, torch.Tensor]] = None,
                  host_output: Optional[torch.Tensor] = None):
         dev = q_lat.device
@@ -85,9 +87,10 @@ class DecodeStep:
         self.host_output = host_output
         self._args = (q_lat, q_rope, latent_cache, rope_cache, block_table, seqlens, scale, out_scale)
         self._w_uv, self._d_h = w_uv, d_h
+        self._latent_scale = latent_scale
         # decode and up-projection in one launch where that kernel covers the
-        # shape (batch <= 64), else the two launches
-        self._fused = w_uv is not None and q_lat.shape[0] <= 64
+        # shape (batch <= 64, a bf16 cache), else the two launches
+        self._fused = w_uv is not None and q_lat.shape[0] <= 64 and latent_scale is None
 
         # validation: one eager pass (raises on any argument error) on the
         # step's real inputs: the host inputs, if any, are brought in first,
@@ -124,7 +127,12 @@ class DecodeStep:
                 b.mlra_decode_up_proj(*self._args, self._w_uv, d_h=self._d_h, out=self.out, y=y_dst,
                                       workspace=self.workspace, stream=stream)
             else:
-                b.mlra_decode(*self._args, out=self.out, workspace=self.workspace, stream=stream)
+                if self._latent_scale is None:
+                    b.mlra_decode(*self._args, out=self.out, workspace=self.workspace, stream=stream)
+                else:
+                    q_lat, q_rope, cache, *rest = self._args
+                    b.mlra_decode_fp8(q_lat, q_rope, cache, self._latent_scale, *rest, out=self.out,
+                                      workspace=self.workspace, stream=stream)
                 if self._w_uv is not None:
                     b.mlra_up_proj(self.out, self._w_uv, d_h=self._d_h, y=y_dst, stream=stream)
             if copies and self.host_output is not None and not direct:

@@ -288,6 +288,110 @@ MLRA_API mlra_status mlra_prepare(const mlra_dims* dims, int32_t d_h, const void
                                   int32_t* device_status, void* stream);
 
 /*
+ * Attention over a prompt: the new tokens of `dims->batch` sequences, packed
+ * one after the other, each attending to its sequence's cached tokens up to
+ * and including itself (causal), every branch on its own ("The Core Insight"
+ * section of the blog page).  Sequence n owns the query rows
+ * [cu_seqlens[n], cu_seqlens[n+1]); with q of them and length L = seqlens[n]
+ * its i-th new token sits at position p = L - q + i, and for every head h and
+ * branch b
+ *   s_t = scale * (q_lat[row,h,b,:] . c_b[t] + q_rope[row,h,:] . k_r[t]),  t = 0 .. p
+ *   out[row,h,b,:] = out_scale * sum_t softmax_t(s)_t * c_b[t]
+ * A whole prompt has q = L, a chunk of one q < L, a decode step q = 1 (there
+ * mlra_decode is the faster call); q = 0 sequences have no rows.  The new
+ * tokens' latents and rotated keys are in the cache already (mlra_prepare
+ * takes a prompt's tokens as its batch).
+ *   tokens       T: rows of q_lat, q_rope and out (0: nothing to do)
+ *   q_lat        bf16 [T, heads, branches, d_c]
+ *   q_rope       bf16 [T, heads, d_r]
+ *   latent_cache bf16 [num_pages, page_size, branches, d_c]
+ *   rope_cache   bf16 [num_pages, page_size, d_r]
+ *   block_table  int32 [batch, max_pages_per_seq]; the first ceil(L/P) entries
+ *                of a row are read
+ *   seqlens      int32 [batch]      lengths including the new tokens
+ *   cu_seqlens   int32 [batch + 1]  non-decreasing, at most T
+ *   out          bf16 [T, heads, branches, d_c]  written; rows of no sequence
+ *                stay as they were
+ *   device_status  optional int32 (device, may be NULL): zeroed, then the
+ *                first device-detected problem.  MLRA_ERR_DEVICE_BAD_SEQLEN:
+ *                L < max(q, 1) or beyond the block table (rows written as
+ *                zeros), or offsets that decrease or leave [0, T] (no rows
+ *                written); MLRA_ERR_DEVICE_BAD_INDEX: a page of the sequence
+ *                outside the pool (rows written as zeros).
+ * Cache slots at or behind L never reach a result, whatever they hold; a
+ * non-finite latent before L reaches the rows of its sequence.
+ * Scores, maxima and sums are fp32; the probabilities enter the output
+ * product as bf16.  Supported shapes as mlra_decode (heads <= 128; tokens *
+ * heads < 2^31).  Allocates nothing.
+ */
+MLRA_API mlra_status mlra_prefill(const mlra_dims* dims, int32_t tokens, const void* q_lat, const void* q_rope,
+                                  const void* latent_cache, const void* rope_cache, const int32_t* block_table,
+                                  const int32_t* seqlens, const int32_t* cu_seqlens, float scale, float out_scale,
+                                  void* out, int32_t* device_status, void* stream);
+
+/*
+ * The 8-bit cache.  Latents are e4m3 values (1 byte: 4 exponent, 3 mantissa
+ * bits, largest 448) with one fp32 scale for every MLRA_FP8_BLOCK tokens of a
+ * page and each branch:
+ *   c_b[t] = latent_scale[page][slot / 16][b] * latent_cache[page][slot][b][:]
+ * RoPE keys stay bf16 (they are an eighth of the values, and an angle's error
+ * grows with the score).  At the 2.9B shape a token takes 641 bytes instead
+ * of 1152.  (The pages describing the method name no such cache.)
+ */
+#define MLRA_FP8_BLOCK 16
+
+/*
+ * Appends a run of new tokens to each sequence's 8-bit cache.  Sequence n's
+ * run is the rows [cu_seqlens[n], cu_seqlens[n+1]) of c_new and kr_new; with
+ * q of them and L = seqlens[n] they become positions L - q .. L - 1.
+ *  - Scale: a block of 16 positions and a branch has the smallest power of
+ *    two sigma with amax <= 448 sigma, at least 2^-40, amax the largest finite
+ *    magnitude of its new values.  A block that holds earlier tokens of the
+ *    sequence keeps the larger of its scale and that one; where it grows, the
+ *    earlier tokens' values are rounded again at the new scale.
+ *  - Values: x / sigma rounded to the nearest e4m3 (ties to even); infinities
+ *    become +-448, NaN stays NaN.
+ *  - Keys: rotated to their positions as mlra_prepare does, bf16.
+ *   dims         as mlra_prepare's (heads is not used)
+ *   tokens       T: rows of c_new and kr_new (0: nothing to do)
+ *   c_new        bf16 [T, branches, d_c]
+ *   kr_new       bf16 [T, d_r]  unrotated
+ *   cu_seqlens   int32 [batch + 1]  non-decreasing, at most T
+ *   seqlens      int32 [batch]      lengths including the runs
+ *   block_table  int32 [batch, max_pages_per_seq]
+ *   latent_cache e4m3 [num_pages, page_size, branches, d_c]       written
+ *   latent_scale fp32 [num_pages, page_size / 16, branches]       written
+ *   rope_cache   bf16 [num_pages, page_size, d_r]                 written
+ *   device_status  optional int32 (device, may be NULL): zeroed, then the
+ *                first device-detected problem: MLRA_ERR_DEVICE_BAD_SEQLEN
+ *                (offsets or length out of range: the run is not written) or
+ *                MLRA_ERR_DEVICE_BAD_INDEX (a page outside the pool: its
+ *                tokens are not written)
+ * Slots that no run covers keep what they hold.  Two runs of one call must
+ * not write the same page.  d_c in {64, 128, 256, 512}, branches <= 8, d_r
+ * even and at most 64, page_size a multiple of 16.  Allocates nothing.
+ */
+MLRA_API mlra_status mlra_append_fp8(const mlra_dims* dims, int32_t tokens, const void* c_new, const void* kr_new,
+                                     const int32_t* cu_seqlens, const int32_t* seqlens,
+                                     const int32_t* block_table, float rope_base, void* latent_cache,
+                                     void* latent_scale, void* rope_cache, int32_t* device_status, void* stream);
+
+/*
+ * mlra_decode over the 8-bit cache: the same arguments, shapes, workspace and
+ * errors, with
+ *   latent_cache e4m3 [num_pages, page_size, branches, d_c]
+ *   latent_scale fp32 [num_pages, page_size / 16, branches], positive and
+ *                finite (mlra_append_fp8 writes powers of two)
+ * The queries, scores, sums and outputs keep mlra_decode's precision: only
+ * the cache is in 8 bits.
+ */
+MLRA_API mlra_status mlra_decode_fp8(const mlra_dims* dims, const void* q_lat, const void* q_rope,
+                                     const void* latent_cache, const void* latent_scale, const void* rope_cache,
+                                     const int32_t* block_table, const int32_t* seqlens, float scale,
+                                     float out_scale, void* out, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/*
  * Branch-sharded tensor parallelism ("The Core Insight" section of the blog
  * page: the branches can be placed on different GPUs, so each GPU reads only
  * its own branches' latents plus the shared RoPE key -- 1.5 d_h per token

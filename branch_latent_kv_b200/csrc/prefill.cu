@@ -1,78 +1,520 @@
 // prefill.cu -- causal attention of packed prompt tokens over the paged
-// latent cache (mlra_prefill): out = out_scale softmax(scale (q_lat . c_b +
-// q_rope . k_r)) c_b over the tokens up to the query's own, every branch on
-// its own.  One warp per (query row, head, branch): a lane owns d_c / 32
-// latent columns and d_r / 32 key columns, and the warp walks the tokens with
-// a running maximum and sum.
+// latent cache, on the sm_100a tensor cores (mlra_prefill).
+//
+// For new token i of a sequence, at position p, head h and branch b
+//   s_t = scale * (q_lat[i,h,b] . c_b[t] + q_rope[i,h] . k_r[t]),  t <= p,
+//   out[i,h,b] = out_scale * sum_t softmax_t(s)_t c_b[t]
+// ("MLRA: Breaking the Sharding Bottleneck in Latent Attention", wispaper.ai
+// blog, section "The Core Insight": every branch is attended independently).
+// All heads of a branch read the same latents, which are keys and values at
+// once, so a branch is one problem with the (token, head) pairs as rows:
+//   S = [Q | Qr] [C | Kr]^T,  O += P C,
+// rows r = i H + h lying in memory at a constant stride whatever H is.
+//
+// One CTA per (128 MT rows of a sequence, branch, VN value columns):
+//   warp 0     copies: Q once, then per tile of KT tokens the latents and the
+//              keys (one TMA box per page, or part of one) into two rings
+//   warp 1     MMAs (tcgen05, one elected thread) and TMEM:
+//                S[slot] = Q C^T + Qr Kr^T   K = d_c + d_r, N = KT
+//                O += P[slot] C              P from TMEM, the same tile of C as
+//                                            MN-major operand, N = VN
+//   others     softmax, one thread per row (a TMEM lane): one pass with a
+//              running maximum and sum; P goes to TMEM as bf16 over the
+//              scores it came from; at the end O / sum is written
+// Two score slots keep the tensor pipe busy while a softmax runs: the two
+// 128-row tiles of a CTA (MT = 2, d_c <= 128) or, where one tile's output
+// fills half of TMEM (MT = 1), two consecutive token tiles.  Work item w uses
+// slot w % 2; PV(w) and then QK(w + 2) are issued when softmax w is done, and
+// because MMAs run in issue order the slot needs no further barrier.
+// The running maximum is raised only when a score exceeds it by 2^8 (a row's
+// O is rescaled then, by the row's own warp, without a barrier between warps).
+//
+// P is rounded to bf16 (the output MMA takes P and C in one type, and C is
+// bf16): half a step, 2^-8 of each probability, averaged over the row; the
+// sum is of the unrounded ones.  Scores, maxima, sums and O are fp32.
 #include "common.cuh"
 #include "kernels.h"
+#include "sm100.cuh"
+#include "tensor_map.cuh"
 
 namespace mlra {
 namespace {
 
-constexpr int kWarps = 4;
+using namespace sm100;
+
+constexpr int kSmemMax = 232448;
+constexpr float kRescale = 8.0f;  // log2 of how far a score may pass the running maximum
 
 template <int DC, int DR>
-__global__ void __launch_bounds__(kWarps * 32) prefill_kernel(const PrefillArgs a) {
-    constexpr int E = DC / 32, ER = DR / 32;
+struct Cfg {
+    static constexpr int MT = DC <= 128 ? 2 : 1;                      // 128-row tiles per CTA
+    static constexpr int KT = DC <= 128 ? 128 : DC == 256 ? 64 : 32;  // tokens per tile
+    static constexpr int VN = DC <= 256 ? DC : 256;                   // value columns per CTA
+    static constexpr int NV = DC / VN;                                // CTAs per row block and branch
+    static constexpr int BM = 128 * MT;
+    static constexpr int NCH = DC / 64;  // 64-column (128-byte) chunks of a latent row
+    static constexpr int Q_CHUNK = 128 * 128;
+    static constexpr int QR_BYTES = 128 * DR * 2;
+    static constexpr int Q_TILE = NCH * Q_CHUNK + QR_BYTES;
+    static constexpr int C_CHUNK = KT * 128;
+    static constexpr int C_BYTES = NCH * C_CHUNK;
+    static constexpr int K_BYTES = KT * DR * 2;
+    static constexpr int MISC = 1024;
+    // ring depths: the tile a PV reads, the one the next QK reads, and what
+    // fits beyond
+    static constexpr int NK = DC == 64 ? 4 : DC == 256 ? 3 : 2;
+    static constexpr int NC_FIT = (kSmemMax - 1024 - MISC - MT * Q_TILE - NK * K_BYTES) / C_BYTES;
+    static constexpr int NC = NC_FIT > 4 ? 4 : NC_FIT;
+    static constexpr int OFF_Q = 0;  // Q tile m: chunks, then its RoPE part
+    static constexpr int OFF_C = MT * Q_TILE;
+    static constexpr int OFF_K = OFF_C + NC * C_BYTES;
+    static constexpr int OFF_MISC = OFF_K + NK * K_BYTES;
+    static constexpr int SMEM = OFF_MISC + MISC + 1024;
+    // TMEM columns: two score slots, then the output tiles
+    static constexpr int S_COLS = KT;
+    static constexpr int O_COL = MT == 2 ? 256 : 2 * S_COLS;
+    static constexpr int TMEM_COLS = O_COL + MT * VN <= 256 ? 256 : 512;
+    static constexpr int SOFT_WARPS = 4 * MT;
+    static constexpr int THREADS = 64 + 32 * SOFT_WARPS;
+    static_assert(NC >= 2 && SMEM <= kSmemMax, "shared memory");
+    static_assert(O_COL + MT * VN <= 512, "TMEM");
+    static_assert(Q_TILE % 1024 == 0 && C_CHUNK % 1024 == 0 && K_BYTES % 1024 == 0, "swizzle atoms stay aligned");
+};
+
+struct Misc {
+    uint64_t c_full[4], c_empty[4];
+    uint64_t k_full[4], k_empty[4];
+    uint64_t s_full[2];   // item w in slot w % 2: its scores are in TMEM
+    uint64_t p_full[2];   // its probabilities are in TMEM
+    uint64_t o_done[2];   // its output MMA has finished
+    uint64_t q_full;
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort_flag;
+    int bad;      // a page of the sequence lies outside the pool
+    int job[5];   // sequence (-1: none), first row in it, rows, first packed row, past (-1: zeros)
+};
+
+struct Maps {
+    CUtensorMap q, qr, lat, rope;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Row blocks ("places") of sequence n start at cu[n] H / BM + n: room for
+// ceil(q H / BM) of them.  In 64 bits, since cu may hold anything.
+__device__ __forceinline__ long long place_of(const PrefillArgs& a, int n, int BM) {
+    const long long rows = (long long)__ldg(a.cu_seqlens + n) * a.heads;
+    return (rows >= 0 ? rows / BM : -((BM - 1 - rows) / BM)) + n;
+}
+
+// Whole warp: the last sequence whose first place is at or before v.
+__device__ __forceinline__ int find_seq(const PrefillArgs& a, long long v, int BM) {
     const int lane = threadIdx.x & 31;
-    const long long item = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int B = a.branches, H = a.heads, P = a.page_size;
-    if (item >= (long long)a.tokens * H * B) return;
-    const int row = (int)(item / (H * B)), h = (int)(item / B) % H, b = (int)(item % B);
-    // the sequence whose run holds this row
-    int n = -1, c0 = 0, q = 0;
-    for (int m = 0; m < a.batch; ++m) {
-        const int lo = a.cu_seqlens[m], hi = a.cu_seqlens[m + 1];
-        if (lo >= 0 && hi >= lo && hi <= a.tokens) {
-            if (row >= lo && row < hi) n = m, c0 = lo, q = hi - lo;
-        } else if (lane == 0 && a.status != nullptr) {
-            record_error(a.status, MLRA_ERR_DEVICE_BAD_SEQLEN);
+    int lo = 0, len = a.batch;  // the answer lies in [lo, lo + len)
+    while (len > 1) {
+        const int step = (len + 31) / 32, n = lo + lane * step, end = lo + len;
+        const unsigned hit = __ballot_sync(0xffffffffu, n < end && place_of(a, n, BM) <= v);
+        lo += (hit ? 31 - __clz(hit) : 0) * step;
+        len = min(step, end - lo);
+    }
+    return lo;
+}
+
+template <int DR>
+__device__ __forceinline__ uint64_t rope_desc(uint32_t addr) {
+    return DR == 64 ? smem_desc(addr, 16, 1024, kLayoutSw128) : smem_desc(addr, 16, 512, kLayoutSw64);
+}
+
+template <int DC, int DR>
+__global__ void __launch_bounds__(Cfg<DC, DR>::THREADS, 1)
+prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ PrefillArgs a, const long long places) {
+    using C = Cfg<DC, DR>;
+    static_assert(sizeof(Misc) <= C::MISC, "barriers fit");
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Misc& misc = *reinterpret_cast<Misc*>(sm + C::OFF_MISC);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int H = a.heads, B = a.branches, P = a.page_size;
+    const int part = blockIdx.x % (B * C::NV), b = part / C::NV, v0 = part % C::NV * C::VN;
+    // a sequence's later row blocks see more tokens: they start first
+    const long long place = places - 1 - blockIdx.x / (B * C::NV);
+
+    launch_dependents();
+    if (threadIdx.x == 32) {
+        for (int i = 0; i < C::NC; ++i) mbar_init(&misc.c_full[i], 1), mbar_init(&misc.c_empty[i], 1);
+        for (int i = 0; i < C::NK; ++i) mbar_init(&misc.k_full[i], 1), mbar_init(&misc.k_empty[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&misc.s_full[i], 1);
+            mbar_init(&misc.p_full[i], 4);
+            mbar_init(&misc.o_done[i], 1);
+        }
+        mbar_init(&misc.q_full, 1);
+        mbar_init(&misc.drain, 1);
+        misc.abort_flag = 0;
+        misc.bad = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tmem_alloc(&misc.tmem_base, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    wait_prerequisite_grid();
+    if (warp == 0) {
+        const int n = find_seq(a, place, C::BM);
+        const int c0 = __ldg(a.cu_seqlens + n), c1 = __ldg(a.cu_seqlens + n + 1), L = __ldg(a.seqlens + n);
+        const bool run = c0 >= 0 && c1 >= c0 && c1 <= a.tokens;
+        const long long row0 = (place - place_of(a, n, C::BM)) * C::BM;
+        const bool mine = run && row0 >= 0 && row0 < (long long)(c1 - c0) * H;
+        const bool good = L >= c1 - c0 && seqlen_valid(L, P, a.max_pages);
+        if (lane == 0) {
+            misc.job[0] = mine ? n : -1;
+            misc.job[1] = mine ? (int)row0 : 0;
+            misc.job[2] = mine ? (c1 - c0) * H : 0;
+            misc.job[3] = mine ? c0 * H : 0;
+            misc.job[4] = good ? L - (c1 - c0) : -1;
+            if (mine && !good && a.status != nullptr) record_error(a.status, MLRA_ERR_DEVICE_BAD_SEQLEN);
         }
     }
-    if (n < 0) return;
-    const int L = a.seqlens[n];
-    int bad = 0;
-    if (L < q || !seqlen_valid(L, P, a.max_pages)) bad = MLRA_ERR_DEVICE_BAD_SEQLEN;
-    const int32_t* bt = a.block_table + (size_t)n * a.max_pages;
-    if (!bad) {
-        bool out = false;
-        for (int i = lane; i < ceil_div(L, P); i += 32) out |= bt[i] < 0 || bt[i] >= a.num_pages;
-        if (__any_sync(0xffffffffu, out)) bad = MLRA_ERR_DEVICE_BAD_INDEX;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const int n = misc.job[0], row0 = misc.job[1], rows = misc.job[2], past = misc.job[4];
+    const size_t out0 = (size_t)misc.job[3] + row0;  // this CTA's first (token, head) row of out
+    const uint32_t tmem = misc.tmem_base;
+    const size_t W = (size_t)B * DC;
+    if (blockIdx.x == 0 && a.status != nullptr) {  // offsets out of range, whichever places they claim
+        for (int m = threadIdx.x; m < a.batch; m += C::THREADS) {
+            const int c0 = __ldg(a.cu_seqlens + m), c1 = __ldg(a.cu_seqlens + m + 1);
+            if (c0 < 0 || c1 < c0 || c1 > a.tokens) record_error(a.status, MLRA_ERR_DEVICE_BAD_SEQLEN);
+        }
     }
-    __nv_bfloat16* dst = a.out + (((size_t)row * H + h) * B + b) * DC;
-    if (bad) {
-        if (lane == 0 && a.status != nullptr) record_error(a.status, bad);
-        for (int j = 0; j < E; ++j) dst[lane + 32 * j] = to_bf16(0.f);
-        return;
+
+    if (n >= 0 && past < 0) {  // a bad length: zeros
+        const int left = min(C::BM, rows - row0);
+        for (int e = threadIdx.x; e < left * (C::VN / 8); e += C::THREADS)
+            *reinterpret_cast<uint4*>(a.out + (out0 + e / (C::VN / 8)) * W + b * DC + v0 + e % (C::VN / 8) * 8) =
+                make_uint4(0u, 0u, 0u, 0u);
+    } else if (n >= 0) {
+        const int last_row = min(row0 + C::BM, rows) - 1;
+        const int kv_end = past + last_row / H + 1;  // tokens that some row sees
+        const int ntiles = ceil_div(kv_end, C::KT), nitems = ntiles * C::MT;
+        const int32_t* bt = a.block_table + (size_t)n * a.max_pages;
+        volatile int* abort_flag = &misc.abort_flag;
+
+        if (warp == 0) {
+            // ------------------------------------------------------------ copies
+            const int box = min(P, C::KT);
+            bool ok = true;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&misc.q_full, C::MT * C::Q_TILE);
+                for (int m = 0; m < C::MT; ++m) {
+                    uint8_t* dst = sm + C::OFF_Q + m * C::Q_TILE;
+                    const int y = (int)out0 + m * 128;
+                    for (int c = 0; c < C::NCH; ++c)
+                        tma_load_2d(dst + c * C::Q_CHUNK, &maps.q, b * DC + c * 64, y, &misc.q_full);
+                    tma_load_2d(dst + C::NCH * C::Q_CHUNK, &maps.qr, 0, y, &misc.q_full);
+                }
+            }
+            int win = 0, page_of_lane = 0;  // 32 block-table entries from `win` on
+            if (lane < a.max_pages) page_of_lane = __ldg(bt + lane);
+            int done = 0;  // tiles whose copies were issued
+            for (int i = 0; i < ntiles && ok; ++i) {
+                const int tok0 = i * C::KT, nbox = ceil_div(min(C::KT, kv_end - tok0), box);
+                const int page0 = tok0 / P;
+                if (page0 + (nbox * box + P - 1) / P > win + 32) {
+                    win = page0;
+                    page_of_lane = win + lane < a.max_pages ? __ldg(bt + win + lane) : 0;
+                }
+                const int cs = i % C::NC, ks = i % C::NK;
+                if (lane == 0) {
+                    if (i >= C::NK) ok = mbar_wait(&misc.k_empty[ks], (i / C::NK - 1) & 1);
+                    if (ok && i >= C::NC) ok = mbar_wait(&misc.c_empty[cs], (i / C::NC - 1) & 1);
+                    ok = ok && !*abort_flag;
+                    if (ok) {
+                        mbar_arrive_expect_tx(&misc.k_full[ks], nbox * box * DR * 2);
+                        mbar_arrive_expect_tx(&misc.c_full[cs], nbox * box * C::NCH * 128);
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                for (int q = 0; q < nbox; ++q) {
+                    const int tok = tok0 + q * box;
+                    int page = __shfl_sync(0xffffffffu, page_of_lane, tok / P - win);
+                    page = page >= 0 && page < a.num_pages ? page : 0;  // (the softmax warps report it)
+                    const int y = page * P + tok % P;
+                    if (lane == 0) {
+                        tma_load_2d(sm + C::OFF_K + ks * C::K_BYTES + q * box * DR * 2, &maps.rope, 0, y, &misc.k_full[ks]);
+                        for (int c = 0; c < C::NCH; ++c)
+                            tma_load_2d(sm + C::OFF_C + cs * C::C_BYTES + c * C::C_CHUNK + q * box * 128, &maps.lat,
+                                        b * DC + c * 64, y, &misc.c_full[cs]);
+                    }
+                }
+                done = i + 1;
+            }
+            if (lane == 0) {
+                if (!ok) *abort_flag = 1;
+                // no copy may land after this CTA has gone
+                mbar_wait(&misc.q_full, 0, 200000000ull);
+                for (int i = max(0, done - C::NK); i < done; ++i)
+                    mbar_wait(&misc.k_full[i % C::NK], (i / C::NK) & 1, 200000000ull);
+                for (int i = max(0, done - C::NC); i < done; ++i)
+                    mbar_wait(&misc.c_full[i % C::NC], (i / C::NC) & 1, 200000000ull);
+            }
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ MMAs
+            constexpr uint32_t ID_S = idesc_bf16_f32(128, C::KT, false, false);
+            constexpr uint32_t ID_O = idesc_bf16_f32(128, C::VN, false, true);
+            const uint32_t base = smem_u32(sm);
+            const uint64_t dQ = smem_desc(base + C::OFF_Q, 16, 1024, kLayoutSw128);
+            const uint64_t dQr = rope_desc<DR>(base + C::OFF_Q + C::NCH * C::Q_CHUNK);
+            const uint64_t dC = smem_desc(base + C::OFF_C, 16, 1024, kLayoutSw128);           // K-major
+            const uint64_t dV = smem_desc(base + C::OFF_C + v0 / 64 * C::C_CHUNK, C::C_CHUNK, 1024, kLayoutSw128);  // MN-major
+            const uint64_t dK = rope_desc<DR>(base + C::OFF_K);
+            bool ok = mbar_wait_warp(&misc.q_full, 0);
+            tc_fence_after();
+            for (int w = -2; w < nitems && ok; ++w) {
+                if (w >= 0) {
+                    // O += P(w) C
+                    const int i = w / C::MT, m = w % C::MT, cs = i % C::NC, slot = w & 1;
+                    ok = mbar_wait_warp(&misc.p_full[slot], (w >> 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t d = tmem + C::O_COL + m * C::VN, p = tmem + slot * C::S_COLS;
+                    const uint64_t v = dV + ((cs * C::C_BYTES) >> 4);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < C::KT / 16; ++k) mma_bf16_ts(d, p + 8 * k, v + (k * 2048 >> 4), ID_O, (i | k) ? 1u : 0u);
+                        mma_commit(&misc.o_done[slot]);
+                        if (m == C::MT - 1) mma_commit(&misc.c_empty[cs]);
+                    }
+                    __syncwarp();
+                }
+                if (w + 2 < nitems) {
+                    // S(w + 2) = Q C^T + Qr Kr^T
+                    const int u = w + 2, i = u / C::MT, m = u % C::MT, cs = i % C::NC, ks = i % C::NK;
+                    if (m == 0) {
+                        ok = mbar_wait_warp(&misc.k_full[ks], (i / C::NK) & 1) && mbar_wait_warp(&misc.c_full[cs], (i / C::NC) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    const uint32_t d = tmem + (u & 1) * C::S_COLS;
+                    const uint64_t q = dQ + ((m * C::Q_TILE) >> 4), c = dC + ((cs * C::C_BYTES) >> 4);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < DR / 16; ++k)
+                            mma_bf16(d, dQr + ((m * C::Q_TILE) >> 4) + 2 * k, dK + ((ks * C::K_BYTES) >> 4) + 2 * k, ID_S, k ? 1u : 0u);
+#pragma unroll
+                        for (int k = 0; k < DC / 16; ++k)
+                            mma_bf16(d, q + ((k / 4 * C::Q_CHUNK) >> 4) + k % 4 * 2, c + ((k / 4 * C::C_CHUNK) >> 4) + k % 4 * 2, ID_S, 1u);
+                        mma_commit(&misc.s_full[u & 1]);
+                        if (m == C::MT - 1) mma_commit(&misc.k_empty[ks]);
+                    }
+                    __syncwarp();
+                }
+                if (__shfl_sync(0xffffffffu, *abort_flag, 0)) ok = false;
+            }
+            if (!ok && lane == 0) *abort_flag = 1;
+            // every MMA has finished before TMEM is freed
+            if (elect_one()) mma_commit(&misc.drain);
+            __syncwarp();
+            mbar_wait(&misc.drain, 0, 200000000ull);
+            __syncwarp();
+        } else {
+            // ------------------------------------------------------------ softmax
+            const int g = (warp - 2) / 4;                 // row tile (MT = 2) of this warpgroup
+            const int quad = warp & 3;                    // TMEM lane quadrant
+            const int r = quad * 32 + lane;               // row within the 128
+            const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+            const uint32_t o_addr = lanes + C::O_COL + g * C::VN;
+            const int row = row0 + g * 128 + r;
+            const int pos = past + min(row, rows - 1) / H;  // last token of this row
+            const int pos_first = past + min(row0 + g * 128 + quad * 32, rows - 1) / H;  // of the warp's first row
+            const float sc = a.scale_log2;
+            const int L = past + rows / H;
+            {
+                // every page of the sequence has to lie in the pool
+                bool bad = false;
+                for (int e = threadIdx.x - 64; e < ceil_div(L, P); e += 32 * C::SOFT_WARPS) {
+                    const int page = __ldg(bt + e);
+                    bad |= page < 0 || page >= a.num_pages;
+                }
+                if (bad) misc.bad = 1;
+            }
+            float mx = -INFINITY, l = 0.f;  // running maximum (log2 units) and sum
+            bool ok = true;
+            int w = g;
+            for (; w < nitems; w += C::MT) {
+                const int i = w / C::MT, slot = w & 1, tok0 = i * C::KT;
+                const uint32_t s_addr = lanes + slot * C::S_COLS;
+                ok = mbar_wait_warp(&misc.s_full[slot], (w >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t x[C::KT];
+#pragma unroll
+                for (int c = 0; c < C::KT / 32; ++c) tmem_ld32(s_addr + 32 * c, x + 32 * c);
+                tmem_wait_ld();
+                reg_tie<C::KT>(x);
+                // tokens j > limit of the tile are masked (a whole warp's rows at once see it all otherwise)
+                const int limit = pos - tok0;
+                const bool diagonal = pos_first - tok0 < C::KT - 1;
+                if (diagonal) {
+                    const uint32_t none = sc < 0.f ? 0x7f800000u : 0xff800000u;
+#pragma unroll
+                    for (int j = 0; j < C::KT; ++j) x[j] = j > limit ? none : x[j];
+                }
+                // the largest scaled score (the smallest raw one under a negative scale)
+                float top[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top[k] = __uint_as_float(x[k]);
+                if (sc < 0.f) {
+#pragma unroll
+                    for (int j = 4; j < C::KT; ++j) top[j & 3] = fminf(top[j & 3], __uint_as_float(x[j]));
+                    top[0] = fminf(fminf(top[0], top[1]), fminf(top[2], top[3])) * sc;
+                } else {
+#pragma unroll
+                    for (int j = 4; j < C::KT; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(x[j]));
+                    top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
+                }
+                if (i == 0) {
+                    mx = top[0];  // token 0 is seen by every row
+                } else {
+                    const bool grow = top[0] > mx + kRescale;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        // O of this warp's rows at the new maximum, once the PV before is done
+                        const int v = w - C::MT;
+                        ok = mbar_wait_warp(&misc.o_done[v & 1], (v >> 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const float alpha = grow ? ex2(mx - top[0]) : 1.f;
+                        if (grow) mx = top[0];
+                        l *= alpha;
+#pragma unroll 1
+                        for (int c = 0; c < C::VN / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(o_addr + 32 * c, o);
+                            tmem_wait_ld();
+                            reg_tie<32>(o);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                            tmem_st32(o_addr + 32 * c, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                float sum[2] = {0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < C::KT; j += 2) {
+                    float p0 = ex2(fmaf(__uint_as_float(x[j]), sc, -mx)), p1 = ex2(fmaf(__uint_as_float(x[j + 1]), sc, -mx));
+                    if (diagonal) p0 = j > limit ? 0.f : p0, p1 = j + 1 > limit ? 0.f : p1;
+                    sum[0] += p0;
+                    sum[1] += p1;
+                    x[j / 2] = pack_bf16(p0, p1);
+                }
+                l += sum[0] + sum[1];
+                if constexpr (C::KT == 32) {
+                    tmem_st16(s_addr, x);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < C::KT / 64; ++c) tmem_st32(s_addr + 32 * c, x + 32 * c);
+                }
+                // slots behind the last token (stale, or another sequence's) become
+                // zero before the output MMA reads them: 0 * NaN is NaN
+                if (tok0 + C::KT > kv_end) {
+                    uint8_t* tile = sm + C::OFF_C + (i % C::NC) * C::C_BYTES;
+                    const int dead = tok0 + C::KT - kv_end, units = dead * 8;
+                    for (int e = r; e < units * C::NCH; e += 128)
+                        *reinterpret_cast<uint4*>(tile + e / units * C::C_CHUNK + (C::KT - dead) * 128 + e % units * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&misc.p_full[slot]);
+            }
+            if (ok) {
+                const int v = w - C::MT;  // this tile's last item
+                ok = mbar_wait_warp(&misc.o_done[v & 1], (v >> 1) & 1);
+                tc_fence_after();
+            }
+            if (!ok && lane == 0) {
+                *abort_flag = 1;
+                if (a.status != nullptr) record_error(a.status, MLRA_ERR_DEVICE_TIMEOUT);
+            }
+            named_bar_sync<1, 32 * C::SOFT_WARPS>();  // every page check is in
+            const bool bad = misc.bad != 0 || !ok;
+            if (misc.bad != 0 && threadIdx.x == 64 && a.status != nullptr) record_error(a.status, MLRA_ERR_DEVICE_BAD_INDEX);
+            const float inv = a.out_scale / l;
+            __nv_bfloat16* dst = a.out + (out0 + g * 128 + r) * W + b * DC + v0;
+#pragma unroll 1
+            for (int c = 0; c < C::VN / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(o_addr + 32 * c, o);
+                tmem_wait_ld();
+                reg_tie<32>(o);
+#pragma unroll
+                for (int j = 0; j < 32; j += 2)
+                    o[j / 2] = bad ? 0u : pack_bf16(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv);
+                if (row < rows) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        *reinterpret_cast<uint4*>(dst + 32 * c + 8 * k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                }
+            }
+            tc_fence_before();
+        }
     }
-    float ql[E], qr[ER], o[E];
-    for (int j = 0; j < E; ++j) ql[j] = __bfloat162float(a.q_lat[(((size_t)row * H + h) * B + b) * DC + lane + 32 * j]), o[j] = 0.f;
-    for (int j = 0; j < ER; ++j) qr[j] = __bfloat162float(a.q_rope[((size_t)row * H + h) * DR + lane + 32 * j]);
-    float m = -INFINITY, l = 0.f;
-    const int last = L - q + (row - c0);
-    for (int t = 0; t <= last; ++t) {
-        const size_t r = (size_t)bt[t / P] * P + t % P;
-        float c[E], s = 0.f;
-        for (int j = 0; j < E; ++j) c[j] = __bfloat162float(a.latent[(r * B + b) * DC + lane + 32 * j]), s = fmaf(ql[j], c[j], s);
-        for (int j = 0; j < ER; ++j) s = fmaf(qr[j], __bfloat162float(a.rope[r * DR + lane + 32 * j]), s);
-        for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-        s *= a.scale_log2;
-        const float mn = fmaxf(m, s), alpha = exp2f(m - mn), p = exp2f(s - mn);
-        m = mn;
-        l = fmaf(l, alpha, p);
-        for (int j = 0; j < E; ++j) o[j] = fmaf(o[j], alpha, p * c[j]);
-    }
-    for (int j = 0; j < E; ++j) dst[lane + 32 * j] = to_bf16(o[j] * a.out_scale / l);
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+template <int DC, int DR>
+cudaError_t launch_cfg(const PrefillArgs& a, cudaStream_t stream) {
+    using C = Cfg<DC, DR>;
+    Maps maps;
+    const uint64_t W = (uint64_t)a.branches * DC, q_rows = (uint64_t)a.tokens * a.heads;
+    const uint64_t rows = (uint64_t)a.num_pages * a.page_size;
+    const uint32_t box = a.page_size < C::KT ? a.page_size : C::KT;
+    if (!encode_rows(&maps.q, a.q_lat, 2, W, q_rows, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_rows(&maps.qr, a.q_rope, 2, DR, q_rows, DR, 128, rope_swizzle(DR)) ||
+        !encode_rows(&maps.lat, a.latent, 2, W, rows, 64, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_rows(&maps.rope, a.rope, 2, DR, rows, DR, box, rope_swizzle(DR)))
+        return cudaErrorInvalidValue;
+    auto kernel = prefill_kernel<DC, DR>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    const long long places = (long long)(q_rows / C::BM) + a.batch;
+    const long long grid = places * a.branches * C::NV;
+    if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, maps, a, places);
 }
 
 template <int DC>
 cudaError_t launch_dc(const PrefillArgs& a, cudaStream_t stream) {
-    const long long items = (long long)a.tokens * a.heads * a.branches;
-    const unsigned grid = (unsigned)((items + kWarps - 1) / kWarps);
-    if (a.d_r == 64) prefill_kernel<DC, 64><<<grid, kWarps * 32, 0, stream>>>(a);
-    else prefill_kernel<DC, 32><<<grid, kWarps * 32, 0, stream>>>(a);
-    return cudaGetLastError();
+    return a.d_r == 64 ? launch_cfg<DC, 64>(a, stream) : launch_cfg<DC, 32>(a, stream);
 }
 
 }  // namespace

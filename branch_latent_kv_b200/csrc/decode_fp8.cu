@@ -1,85 +1,881 @@
-// decode_fp8.cu -- split-free decode over the 8-bit cache (mlra_decode_fp8):
-// mlra_decode with c_b[t] = sigma[t / 16][b] e[t][b].  One CTA per (sequence,
-// head, branch); a lane owns d_c / 32 latent columns, the warps take every
-// eighth token each with a running maximum and sum, and meet at the end.
+// decode_fp8.cu -- split-KV decode over the 8-bit cache on the sm_100a tensor
+// cores (mlra_decode_fp8): mlra_decode with c_b[t] = sigma_b[t / 16] e_b[t],
+// e an e4m3 value.
+//
+// The roles, the split plan and the merge are those of decode_tc.cu (same
+// warps, one persistent CTA per SM); what the 8-bit cache changes:
+//
+// The latents go to the tensor cores as they lie in memory (kind::f8f6f4),
+// so a token costs half the shared-memory reads that bound the MMAs here
+// (M = 128 and few heads: the latents, operand A, are the traffic) and no
+// conversion.  B has to be 8 bits then too, which a query or a probability is
+// not; but N is free until the columns cost as much as A does (N = 64 at
+// M = 128), so each is split into parts that stand side by side in N:
+//  - a query value, scaled so that the sequence's largest is at most 448,
+//    into hi + lo, both e4m3: 4 + 4 significant bits carry bf16's 8; what the
+//    smallest values lose is 2^-10 of a unit of which the largest has 224 or
+//    more, 2^-17.8 of it.  S = S_hi + S_lo, added when the scores are read.
+//  - a probability into three e5m2 parts: each takes the leading 3 bits of
+//    what is left (the upper byte of a half is an e5m2 value), the last one
+//    rounded: 9 significant bits, 2^-9 of it.  e5m2 because its exponent is
+//    fp16's: with the maximum at 2^7 .. 2^15 a weight down to 2^-24 of the
+//    largest is not lost, and long flat tails are made of those.
+// The value scales go into the probabilities:
+//   z_t = log2(e) scale s_t + log2 sigma_t,  w_t = 2^(z_t - M) = p_t sigma_t,
+//   o = sum w_t e_t / l,  l = sum w_t / sigma_t,
+// with M the running reference of the products p sigma, which are what is
+// rounded (a token row's sigma, its logarithm and reciprocal are per-thread
+// scalars).  Sums, references and outputs are fp32.
+//
+// A step of the MMA <-> softmax pipeline is two branches where a branch is at
+// most 128 wide (two per thread and barrier), else one.
 #include <cuda_fp8.h>
 
+#include <cstddef>
+
 #include "common.cuh"
+#include "decode_split.cuh"
 #include "kernels.h"
+#include "sm100.cuh"
+#include "tensor_map.cuh"
 
 namespace mlra {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kHP = 16;       // heads per tile
+constexpr int kHG = 8;        // heads per softmax warpgroup
+constexpr int kSN = 2 * kHP;  // score columns of a branch: hi and lo query parts
+constexpr int kPN = 3 * kHP;  // output columns of a block: three probability parts
+constexpr int kMaxStages = 16;
+// the reference M sits 2^kBase below the largest weight when it is set, and a
+// weight may pass that by 2^kRescaleLog2: at most 2^15, e5m2 holds 1.75 2^15
+constexpr float kBase = 7.0f;
 
-template <int DC, int DR>
-__global__ void __launch_bounds__(kWarps * 32) decode_fp8_kernel(const DecodeArgs a, const float* latent_scale) {
-    constexpr int E = DC / 32, ER = DR / 32;
-    __shared__ float ms[kWarps], ls[kWarps], os[kWarps][DC];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int B = a.branches, H = a.heads, P = a.page_size;
-    const int b = blockIdx.x % B, h = blockIdx.x / B % H, n = blockIdx.x / B / H;
-    const uint8_t* cache = reinterpret_cast<const uint8_t*>(a.latent);
-    const int L = a.seqlens[n];
-    int bad = seqlen_valid(L, P, a.max_pages) ? 0 : MLRA_ERR_DEVICE_BAD_SEQLEN;
-    const int32_t* bt = a.block_table + (size_t)n * a.max_pages;
-    if (!bad) {
-        bool out = false;
-        for (int i = lane; i < ceil_div(L, P); i += 32) out |= bt[i] < 0 || bt[i] >= a.num_pages;
-        if (__any_sync(0xffffffffu, out)) bad = MLRA_ERR_DEVICE_BAD_INDEX;
-    }
-    float ql[E], qr[ER], o[E];
-    for (int j = 0; j < E; ++j) ql[j] = __bfloat162float(a.q_lat[(((size_t)n * H + h) * B + b) * DC + lane + 32 * j]), o[j] = 0.f;
-    for (int j = 0; j < ER; ++j) qr[j] = __bfloat162float(a.q_rope[((size_t)n * H + h) * DR + lane + 32 * j]);
-    float m = -INFINITY, l = 0.f;
-    for (int t = warp; !bad && t < L; t += kWarps) {
-        const size_t r = (size_t)bt[t / P] * P + t % P;
-        const float sigma = latent_scale[r / kFp8Block * B + b];
-        float c[E], s = 0.f;
-        for (int j = 0; j < E; ++j) {
-            __nv_fp8_e4m3 e;
-            e.__x = cache[(r * B + b) * DC + lane + 32 * j];
-            c[j] = sigma * static_cast<float>(e), s = fmaf(ql[j], c[j], s);
-        }
-        for (int j = 0; j < ER; ++j) s = fmaf(qr[j], __bfloat162float(a.rope[r * DR + lane + 32 * j]), s);
-        for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-        s *= a.scale_log2;
-        const float mn = fmaxf(m, s), alpha = exp2f(m - mn), p = exp2f(s - mn);
-        m = mn;
-        l = fmaf(l, alpha, p);
-        for (int j = 0; j < E; ++j) o[j] = fmaf(o[j], alpha, p * c[j]);
-    }
-    if (lane == 0) ms[warp] = m, ls[warp] = l;
-    for (int j = 0; j < E; ++j) os[warp][lane + 32 * j] = o[j];
-    __syncthreads();
-    float mx = -INFINITY, sum = 0.f;
-    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ms[w]);
-    for (int w = 0; w < kWarps; ++w) sum += ls[w] * exp2f(ms[w] - mx);
-    if (bad && threadIdx.x == 0) record_error(a.err, bad);
-    for (int k = threadIdx.x; k < DC; k += kWarps * 32) {
-        float v = 0.f;
-        for (int w = 0; w < kWarps; ++w) v += os[w][k] * exp2f(ms[w] - mx);
-        a.out[(((size_t)n * H + h) * B + b) * DC + k] = to_bf16(bad ? 0.f : v * a.out_scale / sum);
+template <int NB, int DC, int DR>
+struct Cfg {
+    static constexpr int W = NB * DC;                            // latent bytes per token
+    static constexpr int NCH = W / 128;                          // 128-byte chunks of a token row
+    static constexpr int BPC = DC >= 128 ? 1 : 128 / DC;         // branches per chunk
+    static constexpr int SBR = DC > 128 || NB == 1 ? 1 : 2;      // branches per step
+    static constexpr int CPS = SBR * DC / 128;                   // chunks per step
+    static constexpr int NSTEP = NB / SBR;                       // steps per tile
+    static constexpr int CHUNK_BYTES = kT * 128;
+    static constexpr int ROPE_ROW = DR * 2;
+    static constexpr int ROPE_BYTES = kT * ROPE_ROW;
+    static constexpr int Q_CHUNK_BYTES = kSN * 128;
+    static constexpr int Q_BYTES = NCH * Q_CHUNK_BYTES;
+    static constexpr int QR_SPAN = (kHP * ROPE_ROW + 1023) / 1024 * 1024;
+    static constexpr int P_PART_BYTES = kT * kHP;                // one part of one branch
+    static constexpr int P_BRANCH_BYTES = 3 * P_PART_BYTES;
+    static constexpr int P_BYTES = SBR * P_BRANCH_BYTES;
+    static constexpr int MISC_BYTES = 4096;
+    // steps between their score MMA and their output MMA; RoPE tiles in
+    // flight (three where a tile is one chunk or two); RoPE score slots
+    static constexpr int NSP = NSTEP == 1 && CPS == 1 ? 4 : 3;
+    static constexpr int NROPE = NCH >= 4 ? 2 : NCH == 2 ? 3 : 4;
+    static constexpr int NRS = (NSP + NSTEP - 1) / NSTEP > 2 ? (NSP + NSTEP - 1) / NSTEP : 2;
+    static constexpr int FIXED = NROPE * ROPE_BYTES + Q_BYTES + QR_SPAN + NSP * P_BYTES + MISC_BYTES;
+    static constexpr int NSTAGE_FIT = (kSmemLimit - 1024 - FIXED) / CHUNK_BYTES;
+    static constexpr int NSTAGE = NSTAGE_FIT > kMaxStages ? kMaxStages : NSTAGE_FIT;
+    static constexpr int OFF_CHUNK = 0;
+    static constexpr int OFF_ROPE = OFF_CHUNK + NSTAGE * CHUNK_BYTES;
+    static constexpr int OFF_Q = OFF_ROPE + NROPE * ROPE_BYTES;
+    static constexpr int OFF_QR = OFF_Q + Q_BYTES;
+    static constexpr int OFF_P = OFF_QR + QR_SPAN;
+    static constexpr int OFF_MISC = OFF_P + NSP * P_BYTES;
+    static constexpr int SMEM_BYTES = OFF_MISC + MISC_BYTES + 1024;
+    // TMEM columns: output blocks, score slots, RoPE score slots
+    static constexpr int O_BLOCKS = NCH * BPC;
+    static constexpr int S_COL0 = O_BLOCKS * kPN;
+    static constexpr int S_SLOT_COLS = SBR * kSN;
+    static constexpr int R_COL0 = S_COL0 + NSP * S_SLOT_COLS;
+    static constexpr int COLS = R_COL0 + NRS * kHP;
+    static constexpr int TMEM_COLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+    static_assert(NB % SBR == 0 && SBR * DC % 128 == 0 && NSTEP * CPS == NCH, "steps fill whole chunks");
+    static_assert(NSTAGE >= 2 * CPS && NROPE <= 4 && NSP <= 4, "rings");
+    static_assert(COLS <= 512 && SMEM_BYTES <= kSmemLimit, "TMEM and shared memory");
+    static_assert(Q_BYTES % 1024 == 0 && ROPE_BYTES % 1024 == 0 && P_BYTES % 1024 == 0, "regions stay aligned");
+};
+
+struct Misc {
+    uint64_t chunk_full[kMaxStages];
+    uint64_t chunk_empty[kMaxStages];
+    uint64_t rope_full[4];
+    uint64_t rope_empty[4];
+    uint64_t s_full[4];   // step g in slot g % NSP: its scores are in TMEM
+    uint64_t p_full[4];   // its probabilities are in shared memory
+    uint64_t p_empty[4];  // its output MMA finished
+    uint64_t q_full;      // a range's queries are in shared memory (written by the softmax warps)
+    uint64_t drain[2];
+    uint64_t merge_full;
+    uint32_t tmem_base;
+    int abort_flag;
+    int plan[4];
+    int last_seg[4];
+    int merge_flag;
+    float q_max[8];                   // largest query magnitude seen by each softmax warp
+    float red_max[4][2 * kHP];        // [quadrant][step branch, head]
+    float red_sum[4][4 * kHP];        // [quadrant][group, branch, head]
+    alignas(16) float m_run[4 * kHP]; // reference M per (branch, head)
+    float inv_l[4 * kHP];
+};
+static_assert(offsetof(Misc, m_run) % 16 == 0, "float4 access to m_run");
+
+struct Maps {
+    CUtensorMap lat;   // latent bytes [pages * P][W]
+    CUtensorMap rope;  // RoPE keys [pages * P][d_r]
+};
+
+__device__ __forceinline__ float fast_log2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(float x, float y) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t v) {
+    return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)v, __NV_E4M3)));
+}
+
+// Two fp32 values as a pair of halves.
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// What a pair of halves has beyond its upper bytes (exact).
+__device__ __forceinline__ uint32_t half_rest(uint32_t h) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(h & 0xff00ff00u));
+    return r;
+}
+// The upper bytes of four halves.
+__device__ __forceinline__ uint32_t upper_bytes(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7531); }
+
+// The scales of one token row, every branch (one 16-token block of its page).
+template <int NB>
+__device__ __forceinline__ void load_scales(const float* p, float (&s)[NB]) {
+    if constexpr (NB == 4) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(p));
+        s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
+    } else if constexpr (NB == 2) {
+        const float2 v = __ldg(reinterpret_cast<const float2*>(p));
+        s[0] = v.x, s[1] = v.y;
+    } else {
+        s[0] = __ldg(p);
     }
 }
 
-template <int DC>
-cudaError_t launch_dc(const DecodeArgs& a, const float* s, cudaStream_t stream) {
-    const unsigned grid = (unsigned)a.batch * a.heads * a.branches;
-    if (a.d_r == 64) decode_fp8_kernel<DC, 64><<<grid, kWarps * 32, 0, stream>>>(a, s);
-    else decode_fp8_kernel<DC, 32><<<grid, kWarps * 32, 0, stream>>>(a, s);
-    return cudaGetLastError();
+template <int NB, int DC, int DR>
+__global__ void __launch_bounds__(kThreads, 1)
+decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ DecodeArgs a,
+                  const float* __restrict__ latent_scale) {
+    using C = Cfg<NB, DC, DR>;
+    static_assert(sizeof(Misc) <= C::MISC_BYTES, "barriers and scratch fit the MISC region");
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Misc& misc = *reinterpret_cast<Misc*>(sm + C::OFF_MISC);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int P = a.page_size;
+    const HeadGroup grp = head_group<kHP>(a);
+
+    if (warp == 0 && lane < 2) prefetch_tensormap(lane == 0 ? &maps.lat : &maps.rope);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::NSTAGE; ++i) mbar_init(&misc.chunk_full[i], 1), mbar_init(&misc.chunk_empty[i], 1);
+        for (int i = 0; i < C::NROPE; ++i) mbar_init(&misc.rope_full[i], 1), mbar_init(&misc.rope_empty[i], 1);
+        for (int i = 0; i < C::NSP; ++i) {
+            mbar_init(&misc.s_full[i], 1);
+            mbar_init(&misc.p_full[i], 8);
+            mbar_init(&misc.p_empty[i], 1);
+        }
+        mbar_init(&misc.q_full, 8);
+        mbar_init(&misc.drain[0], 1);
+        mbar_init(&misc.drain[1], 1);
+        mbar_init(&misc.merge_full, 1);
+        misc.abort_flag = 0;
+        misc.last_seg[0] = -1;
+        misc.merge_flag = 0;
+        fence_barrier_init();
+    }
+    launch_dependents();
+    // warp 0 computes the plan and goes on to its copies; the others meet it
+    int n_first, cum_first;
+    if (warp == 0) {
+        wait_prerequisite_grid();
+        const int total = warp_cost_prefix(a.seqlens, a.batch, P, a.max_pages);
+        const int chunk = plan_chunk(total, grp.cpg);
+        n_first = a.batch;
+        cum_first = total;
+        if (!grp.idle && (long long)grp.ci * chunk < total)
+            warp_find_seq(a.seqlens, a.batch, P, a.max_pages, grp.ci * chunk, &n_first, &cum_first);
+        if (lane == 0) {
+            misc.plan[1] = chunk;
+            misc.plan[2] = n_first;
+            misc.plan[3] = cum_first;
+        }
+        __syncwarp();
+        named_bar_arrive<2, kThreads>();
+    } else {
+        if (warp == 1) {
+            tmem_alloc(&misc.tmem_base, C::TMEM_COLS);
+            tmem_relinquish();
+        }
+        tc_fence_before();
+        named_bar_sync<2, kThreads>();
+        tc_fence_after();
+        wait_prerequisite_grid();
+        n_first = misc.plan[2];
+        cum_first = misc.plan[3];
+        if (warp == 6) {
+            // sequences with an invalid length: zeros and an error code
+            for (int m = blockIdx.x; m < a.batch; m += a.num_ctas) {
+                if (seq_tiles(__ldg(a.seqlens + m), P, a.max_pages) > 0) continue;
+                uint4* dst = reinterpret_cast<uint4*>(a.out + (size_t)m * a.heads * C::W);
+                for (int e = lane; e < a.heads * C::W / 8; e += 32) dst[e] = make_uint4(0u, 0u, 0u, 0u);
+                if (lane == 0) record_error(a.err, MLRA_ERR_DEVICE_BAD_SEQLEN);
+            }
+        }
+    }
+    const int chunk = misc.plan[1];
+    const int A0 = grp.ci * chunk, A1 = A0 + chunk;  // this CTA's cost window
+    const uint32_t tmem = misc.tmem_base;            // (warp 0 never uses it)
+    volatile int* abort_flag = &misc.abort_flag;
+
+    if (n_first < a.batch) {
+        int n = n_first, cum = cum_first, next_len = first_len(a, n);
+        int L, tiles, tb, te;
+        if (warp == 0) {
+            // ------------------------------------------------------------ producer
+            uint32_t cc = 0, tc = 0;  // chunks and tiles issued
+            const uint64_t policy = grp.cpg == a.num_ctas ? l2_policy_evict_first() : l2_policy_evict_normal();
+            bool ok = true;
+            while (ok && next_segment(a, n, cum, A0, A1, L, tiles, tb, te, next_len)) {
+                const int32_t* bt = a.block_table + (size_t)n * a.max_pages;
+                int win_base = tb * kT / P, win_val = 0;  // 32 block-table entries, one per lane
+                if (win_base + lane < a.max_pages) win_val = __ldg(bt + win_base + lane);
+                win_val = (win_val >= 0 && win_val < a.num_pages) ? win_val : 0;  // (the softmax warps report bad ones)
+                for (int j = tb; j < te && ok; ++j) {
+                    const int tok0 = j * kT;
+                    const int npages = ceil_div(min(kT, L - tok0), P);
+                    const int page0 = tok0 / P;
+                    if (page0 + npages > win_base + 32) {
+                        win_base = page0;
+                        const int v = page0 + lane < a.max_pages ? __ldg(bt + page0 + lane) : 0;
+                        win_val = (v >= 0 && v < a.num_pages) ? v : 0;
+                    }
+                    const int rs = tc % C::NROPE;
+                    if (lane == 0) {
+                        if (tc >= (uint32_t)C::NROPE) ok = mbar_wait(&misc.rope_empty[rs], ((tc / C::NROPE) - 1) & 1);
+                        if (ok) mbar_arrive_expect_tx(&misc.rope_full[rs], npages * P * C::ROPE_ROW);
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) break;
+                    for (int q = 0; q < npages; ++q) {
+                        const int page = __shfl_sync(0xffffffffu, win_val, page0 + q - win_base);
+                        if (lane == 0)
+                            tma_load_2d_hint(sm + C::OFF_ROPE + rs * C::ROPE_BYTES + q * P * C::ROPE_ROW, &maps.rope, 0,
+                                             page * P, &misc.rope_full[rs], policy);
+                    }
+                    ++tc;
+                    for (int c = 0; c < C::NCH && ok; ++c) {
+                        const int stage = cc % C::NSTAGE;
+                        if (lane == 0) {
+                            ok = mbar_wait(&misc.chunk_empty[stage], ((cc / C::NSTAGE) & 1) ^ 1);
+                            if (ok) mbar_arrive_expect_tx(&misc.chunk_full[stage], npages * P * 128);
+                        }
+                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                        if (!ok) break;
+                        for (int q = 0; q < npages; ++q) {
+                            const int page = __shfl_sync(0xffffffffu, win_val, page0 + q - win_base);
+                            if (lane == 0)
+                                tma_load_2d_hint(sm + C::OFF_CHUNK + stage * C::CHUNK_BYTES + q * P * 128, &maps.lat, c * 128,
+                                                 page * P, &misc.chunk_full[stage], policy);
+                        }
+                        ++cc;
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok && !*abort_flag, 0);
+                }
+                finish_segment(n, cum, tiles);
+            }
+            if (lane == 0) {
+                if (!ok) {
+                    record_error(a.err, MLRA_ERR_DEVICE_TIMEOUT);
+                    *abort_flag = 1;
+                }
+                // no copy may land after this CTA has exited
+                for (uint32_t i = 0; i < (uint32_t)C::NSTAGE && i < cc; ++i) {
+                    const uint32_t k = cc - 1 - i;
+                    mbar_wait(&misc.chunk_full[k % C::NSTAGE], (k / C::NSTAGE) & 1, 200000000ull);
+                }
+                for (uint32_t i = 0; i < (uint32_t)C::NROPE && i < tc; ++i) {
+                    const uint32_t k = tc - 1 - i;
+                    mbar_wait(&misc.rope_full[k % C::NROPE], (k / C::NROPE) & 1, 200000000ull);
+                }
+            }
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ score MMAs
+            constexpr uint32_t ID_S = idesc_f8_f32(128, kSN, kE4M3, kE4M3, false, false);
+            constexpr uint32_t ID_R = idesc_bf16_f32(128, kHP, false, false);
+            const uint32_t base = smem_u32(sm);
+            const uint64_t dA = smem_desc(base + C::OFF_CHUNK, 16, 1024, kLayoutSw128);  // K-major
+            const uint64_t dQ = smem_desc(base + C::OFF_Q, 16, 1024, kLayoutSw128);
+            const uint64_t dQR = rope_desc<DR>(base + C::OFF_QR);
+            const uint64_t dR = rope_desc<DR>(base + C::OFF_ROPE);
+            uint32_t gs = 0, tc = 0, sc = 0, stage = 0, phase = 0;
+            bool ok = true;
+            while (ok && next_segment(a, n, cum, A0, A1, L, tiles, tb, te, next_len)) {
+                ok = mbar_wait_warp(&misc.q_full, sc & 1);
+                tc_fence_after();
+                for (int j = tb; j < te && ok; ++j) {
+                    const uint32_t rs = tc % C::NROPE;
+                    ok = mbar_wait_warp(&misc.rope_full[rs], (tc / C::NROPE) & 1);
+#pragma unroll 1
+                    for (int st = 0; st < C::NSTEP && ok; ++st) {
+                        ok = mbar_wait_warp(&misc.chunk_full[stage], phase);
+                        const uint32_t slot = gs % C::NSP;
+                        if (ok && gs >= (uint32_t)C::NSP) ok = mbar_wait_warp(&misc.p_empty[slot], ((gs / C::NSP) - 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (st == 0) {
+                            // RoPE score of the tile, shared by every branch
+                            const uint32_t d = tmem + C::R_COL0 + (tc % C::NRS) * kHP;
+                            const uint64_t k0 = dR + ((rs * C::ROPE_BYTES) >> 4);
+#pragma unroll
+                            for (int kk = 0; kk < DR / 16; ++kk)
+                                if (elect_one()) mma_bf16(d, k0 + kk * 2, dQR + kk * 2, ID_R, kk ? 1u : 0u);
+                            if (elect_one()) mma_commit(&misc.rope_empty[rs]);
+                            __syncwarp();
+                        }
+                        const uint32_t dS = tmem + C::S_COL0 + slot * C::S_SLOT_COLS;
+#pragma unroll 1
+                        for (int c = 0; c < C::CPS && ok; ++c) {
+                            if (c > 0) {
+                                ok = mbar_wait_warp(&misc.chunk_full[stage], phase);
+                                if (!ok) break;
+                                tc_fence_after();
+                            }
+                            const uint64_t a0 = dA + ((stage * C::CHUNK_BYTES) >> 4);
+                            const uint64_t q0 = dQ + (((st * C::CPS + c) * C::Q_CHUNK_BYTES) >> 4);
+                            // 32 bytes (K) at a time; the chunk's branch (or, of two, the one of its half)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) {
+                                const int g = DC == 64 ? kk / 2 : DC == 128 ? c : 0;
+                                const bool first = DC == 64 ? kk % 2 == 0 : DC == 128 ? kk == 0 : (c | kk) == 0;
+                                if (elect_one()) mma_f8(dS + g * kSN, a0 + kk * 2, q0 + kk * 2, ID_S, first ? 0u : 1u);
+                            }
+                            if (++stage == (uint32_t)C::NSTAGE) stage = 0, phase ^= 1;
+                        }
+                        if (!ok) break;
+                        if (elect_one()) mma_commit(&misc.s_full[slot]);
+                        __syncwarp();
+                        ++gs;
+                    }
+                    ++tc;
+                    if (__shfl_sync(0xffffffffu, *abort_flag, 0)) ok = false;
+                }
+                ++sc;
+                finish_segment(n, cum, tiles);
+            }
+            if (!ok && lane == 0) {
+                record_error(a.err, MLRA_ERR_DEVICE_TIMEOUT);
+                *abort_flag = 1;
+            }
+            if (elect_one()) mma_commit(&misc.drain[0]);
+            __syncwarp();
+            mbar_wait(&misc.drain[0], 0, 200000000ull);
+            __syncwarp();
+        } else if (warp == 6) {
+            // ------------------------------------------------------------ output MMAs
+            constexpr uint32_t ID_O = idesc_f8_f32(128, kPN, kE4M3, kE5M2, true, true);
+            const uint32_t base = smem_u32(sm);
+            // A: the chunk as [128 latent columns][tokens], MN-major (a token row is one
+            // 128-byte swizzle row); B: 16 heads x 8 tokens core matrices, MN-major
+            const uint64_t dA = smem_desc(base + C::OFF_CHUNK, C::CHUNK_BYTES, 1024, kLayoutSw128);
+            const uint64_t dP = smem_desc(base + C::OFF_P, 128, C::P_PART_BYTES, kLayoutNone);
+            uint32_t gs = 0, stage = 0;
+            bool ok = true;
+            while (ok && next_segment(a, n, cum, A0, A1, L, tiles, tb, te, next_len)) {
+                for (int j = tb; j < te && ok; ++j) {
+#pragma unroll 1
+                    for (int st = 0; st < C::NSTEP; ++st) {
+                        const uint32_t slot = gs % C::NSP;
+                        ok = mbar_wait_warp(&misc.p_full[slot], (gs / C::NSP) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t b0 = dP + ((slot * C::P_BYTES) >> 4);
+#pragma unroll
+                        for (int c = 0; c < C::CPS; ++c) {
+                            const uint64_t a0 = dA + ((stage * C::CHUNK_BYTES) >> 4);
+#pragma unroll
+                            for (int g2 = 0; g2 < C::BPC; ++g2) {
+                                // branch of the step whose P multiplies this chunk (the rows of a
+                                // shared chunk's other branch are left out later)
+                                const int g = DC == 64 ? g2 : DC == 128 ? c : 0;
+                                const uint32_t d = tmem + ((st * C::CPS + c) * C::BPC + g2) * kPN;
+#pragma unroll
+                                for (int kt = 0; kt < kT / 32; ++kt)
+                                    if (elect_one())
+                                        mma_f8(d, a0 + (kt * 4096 >> 4), b0 + ((g * C::P_BRANCH_BYTES + kt * 512) >> 4), ID_O,
+                                               (j == tb && kt == 0) ? 0u : 1u);
+                            }
+                            if (elect_one()) mma_commit(&misc.chunk_empty[stage]);
+                            if (++stage == (uint32_t)C::NSTAGE) stage = 0;
+                        }
+                        if (elect_one()) mma_commit(&misc.p_empty[slot]);
+                        __syncwarp();
+                        ++gs;
+                    }
+                    if (__shfl_sync(0xffffffffu, *abort_flag, 0)) ok = false;
+                }
+                finish_segment(n, cum, tiles);
+            }
+            if (!ok && lane == 0) {
+                record_error(a.err, MLRA_ERR_DEVICE_TIMEOUT);
+                *abort_flag = 1;
+            }
+            if (elect_one()) mma_commit(&misc.drain[1]);
+            __syncwarp();
+            mbar_wait(&misc.drain[1], 0, 200000000ull);
+            __syncwarp();
+        } else {
+            // ------------------------------------------------------------ queries, softmax, epilogue
+            const int sg = warp >= 7;                        // softmax group: heads [8 sg, 8 sg + 8)
+            const int hoff = kHG * sg;
+            const uint32_t gbar = 3 + sg;                    // its named barrier (128 threads)
+            const int quad = warp & 3;                       // TMEM lane quadrant
+            const int row = quad * 32 + lane;                // token (S) / latent column (O)
+            const int stid = (warp - (sg ? 7 : 2)) * 32 + lane;
+            const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+            const int H = a.heads;
+            uint32_t gs = 0, tcnt = 0;
+            float l[NB][kHG];
+            bool dead = false;
+            int pend_a = -1, pend_b = -1;
+
+            // (both groups walk every range, so that they meet at the barrier
+            // below even when one has given up; then both stop)
+            for (; next_segment(a, n, cum, A0, A1, L, tiles, tb, te, next_len); finish_segment(n, cum, tiles)) {
+                // ---------------------------------------------------- queries
+                // (the range before has no score MMA left: this thread has seen
+                // its last scores).  16 head rows; heads past the last are zero.
+                float alpha_q;  // a score of the MMA times this is in log2 units (without sigma)
+                {
+                    constexpr int UPR = C::W / 8;               // 8-value units per head row
+                    constexpr int U = kHP * UPR / 256 > 0 ? kHP * UPR / 256 : 1;
+                    const int sid = sg * 128 + stid;
+                    const __nv_bfloat16* q = a.q_lat + ((size_t)n * H + grp.h0) * C::W;
+                    uint4 v[U];
+                    uint32_t mx = 0;
+#pragma unroll
+                    for (int i = 0; i < U; ++i) {
+                        const int u = sid + 256 * i;
+                        v[i] = u / UPR < grp.hn ? __ldg(reinterpret_cast<const uint4*>(q + (size_t)(u / UPR) * C::W) + u % UPR)
+                                                : make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    constexpr int RU = DR / 8;                  // 16-byte units of a RoPE row
+                    if (sid < kHP * RU) {
+                        const int h = sid / RU, u = sid % RU;
+                        const uint4 w = h < grp.hn ? __ldg(reinterpret_cast<const uint4*>(a.q_rope + ((size_t)n * H + grp.h0 + h) * DR) + u)
+                                                   : make_uint4(0u, 0u, 0u, 0u);
+                        const int at = DR == 64 ? h * 128 + ((u ^ (h & 7)) << 4) : h * 64 + ((u ^ ((h >> 1) & 3)) << 4);
+                        *reinterpret_cast<uint4*>(sm + C::OFF_QR + at) = w;
+                    }
+#pragma unroll
+                    for (int i = 0; i < U; ++i) {
+                        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t lo = w[k] & 0x7fffu, hi = (w[k] >> 16) & 0x7fffu;
+                            mx = max(mx, lo < 0x7f80u ? lo : 0u);
+                            mx = max(mx, hi < 0x7f80u ? hi : 0u);
+                        }
+                    }
+                    mx = __reduce_max_sync(0xffffffffu, mx);
+                    if (lane == 0) misc.q_max[sg * 4 + (warp - (sg ? 7 : 2))] = __uint_as_float(mx << 16);
+                    if (named_bar_or<5, 256>(dead)) {
+                        dead = true;
+                        break;
+                    }
+                    float top = misc.q_max[0];
+#pragma unroll
+                    for (int i = 1; i < 8; ++i) top = fmaxf(top, misc.q_max[i]);
+                    // the smallest power of two tau with top <= 448 tau (2^-100 at least: both it
+                    // and its reciprocal are normal numbers)
+                    const uint32_t tb32 = __float_as_uint(top);
+                    const int e = max((int)(tb32 >> 23) - 135 + ((tb32 & 0x7fffffu) > 0x600000u), -100);
+                    const float inv_tau = __uint_as_float((uint32_t)(127 - e) << 23);
+                    alpha_q = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+                    for (int i = 0; i < U; ++i) {
+                        const int u = sid + 256 * i, h = u / UPR, col = u % UPR * 8;
+                        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float x = __uint_as_float(w[k] << 16) * inv_tau, y = __uint_as_float(w[k] & 0xffff0000u) * inv_tau;
+                            x = fmaf(x, 0.f, x);  // infinities become NaN: the head's scores are NaN as in full precision
+                            y = fmaf(y, 0.f, y);
+                            hi[k] = e4m3x2(x, y);
+                            const float2 f = from_e4m3x2(hi[k]);
+                            lo[k] = e4m3x2(x - f.x, y - f.y);
+                        }
+                        if (U * 256 == kHP * UPR || u < kHP * UPR) {
+                            uint8_t* dst = sm + C::OFF_Q + col / 128 * C::Q_CHUNK_BYTES + h * 128 +
+                                           (((col % 128 / 16) ^ (h & 7)) << 4) + col % 16;
+                            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+                            *reinterpret_cast<uint2*>(dst + kHP * 128) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&misc.q_full);
+                }
+                bool bad = false;
+                const int32_t* bt = a.block_table + (size_t)n * a.max_pages;
+                int c1_member = 1;  // as in decode_tc.cu: whether the owner of the last tile merges
+                if (sg == 0 && stid == 0) {
+                    const int c1 = (cum + (tiles - 1) * kTileCost) / chunk;
+                    for (int m = n + 1; m < a.batch; ++m) {
+                        if (seq_tiles(__ldg(a.seqlens + m), a.page_size, a.max_pages) == 0) continue;
+                        c1_member = (cum + tiles * kTileCost + kSeqCost) / chunk != c1;
+                        break;
+                    }
+                }
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int i = 0; i < kHG; ++i) l[b][i] = 0.f;
+
+                // this thread's token: its page one tile ahead, its scales with it
+                auto page_of = [&](int j) { return j < te && j * kT + row < L ? __ldg(bt + (j * kT + row) / P) : 0; };
+                auto scales_of = [&](int page, int j, float (&s)[NB]) {
+                    const bool real = page >= 0 && page < a.num_pages;
+                    load_scales<NB>(latent_scale + ((size_t)(real ? page : 0) * P + (j * kT + row) % P) / kFp8Block * NB, s);
+                    return real;
+                };
+                float sig[NB], sig_next[NB];
+                int page_next = page_of(tb + 1);
+                bad |= !scales_of(page_of(tb), tb, sig);
+
+                for (int j = tb; j < te && !dead; ++j) {
+                    const bool masked = j * kT + row >= L;
+                    const int page_after = page_of(j + 2);
+                    if (j + 1 < te) bad |= !scales_of(page_next, j + 1, sig_next);
+                    page_next = page_after;
+                    float r[kHG];  // this token's RoPE score per head in log2 units
+#pragma unroll
+                    for (int st = 0; st < C::NSTEP; ++st) {
+                        const uint32_t slot = gs % C::NSP;
+                        const bool ok = mbar_wait(&misc.s_full[slot], (gs / C::NSP) & 1);
+                        tc_fence_after();
+                        float z[C::SBR][kHG], low[C::SBR][kHG];
+                        if (st == 0) tmem_ld8(tmem + lane_off + C::R_COL0 + (tcnt % C::NRS) * kHP + hoff, r);
+#pragma unroll
+                        for (int g = 0; g < C::SBR; ++g) {
+                            const uint32_t at = tmem + lane_off + C::S_COL0 + slot * C::S_SLOT_COLS + g * kSN + hoff;
+                            tmem_ld8(at, z[g]);
+                            tmem_ld8(at + kHP, low[g]);
+                        }
+                        tmem_wait_ld();
+                        if (st == 0) {
+#pragma unroll
+                            for (int i = 0; i < kHG; ++i) r[i] *= a.scale_log2;
+                        }
+                        float rs[C::SBR];  // 1 / sigma
+#pragma unroll
+                        for (int g = 0; g < C::SBR; ++g) {
+                            const float s = sig[st * C::SBR + g], ls = fast_log2(s), k = s * alpha_q;
+                            rs[g] = masked ? 0.f : __frcp_rn(s);
+#pragma unroll
+                            for (int i = 0; i < kHG; ++i)
+                                z[g][i] = masked ? -INFINITY : fmaf(z[g][i] + low[g][i], k, r[i] + ls);
+                        }
+                        float* m_step = &misc.m_run[st * C::SBR * kHP + hoff];  // [g * kHP + i]
+                        if (j == tb) {
+                            // the range's first token (always there) sets the references
+                            if (stid == 0) {
+#pragma unroll
+                                for (int g = 0; g < C::SBR; ++g)
+#pragma unroll
+                                    for (int i = 0; i < kHG; ++i) m_step[g * kHP + i] = z[g][i] - kBase;
+                            }
+                            named_bar_sync_id<128>(gbar);
+                        }
+                        float m[C::SBR][kHG];
+#pragma unroll
+                        for (int g = 0; g < C::SBR; ++g)
+#pragma unroll
+                            for (int i = 0; i < kHG; i += 4) {
+                                const float4 v = *reinterpret_cast<const float4*>(m_step + g * kHP + i);
+                                m[g][i] = v.x;
+                                m[g][i + 1] = v.y;
+                                m[g][i + 2] = v.z;
+                                m[g][i + 3] = v.w;
+                            }
+                        bool need = false;
+#pragma unroll
+                        for (int g = 0; g < C::SBR; ++g)
+#pragma unroll
+                            for (int i = 0; i < kHG; ++i) need |= z[g][i] > m[g][i] + (kBase + kRescaleLog2);
+                        if (named_bar_or_id<128>(gbar, need || !ok)) {
+                            if (named_bar_or_id<128>(gbar, !ok)) {
+                                dead = true;
+                                break;
+                            }
+                            // exact column maxima of the tile, new references, O and l at them
+#pragma unroll
+                            for (int g = 0; g < C::SBR; ++g) {
+                                const float v = warp_colmax8(z[g], lane);
+                                if ((lane & 3) == 0) misc.red_max[quad][g * kHP + hoff + lane / 4] = v;
+                            }
+                            named_bar_sync_id<128>(gbar);
+                            float alpha[C::SBR][kHG];
+#pragma unroll
+                            for (int g = 0; g < C::SBR; ++g)
+#pragma unroll
+                                for (int i = 0; i < kHG; ++i) {
+                                    const int c = g * kHP + hoff + i;
+                                    const float top = fmaxf(fmaxf(misc.red_max[0][c], misc.red_max[1][c]),
+                                                            fmaxf(misc.red_max[2][c], misc.red_max[3][c]));
+                                    const float mnew = fmaxf(m[g][i], top - kBase);
+                                    alpha[g][i] = fast_exp2(m[g][i] - mnew);
+                                    m[g][i] = mnew;
+                                    l[st * C::SBR + g][i] *= alpha[g][i];
+                                }
+                            // (everyone has read the old references before the barrier above)
+                            if (stid == 0) {
+#pragma unroll
+                                for (int g = 0; g < C::SBR; ++g)
+#pragma unroll
+                                    for (int i = 0; i < kHG; ++i) m_step[g * kHP + i] = m[g][i];
+                            }
+                            named_bar_sync_id<128>(gbar);
+                            if (j > tb) {
+                                const bool ok2 = mbar_wait(&misc.p_empty[(gs - 1) % C::NSP], ((gs - 1) / C::NSP) & 1);
+                                if (named_bar_or_id<128>(gbar, !ok2)) {
+                                    dead = true;
+                                    break;
+                                }
+                                tc_fence_after();
+#pragma unroll
+                                for (int c = 0; c < C::CPS; ++c)
+#pragma unroll
+                                    for (int g2 = 0; g2 < C::BPC; ++g2) {
+                                        const int g = DC == 64 ? g2 : DC == 128 ? c : 0;
+#pragma unroll
+                                        for (int part = 0; part < 3; ++part) {
+                                            const uint32_t col = ((st * C::CPS + c) * C::BPC + g2) * kPN + part * kHP + hoff;
+                                            float o[kHG];
+                                            tmem_ld8(tmem + lane_off + col, o);
+                                            tmem_wait_ld();
+#pragma unroll
+                                            for (int i = 0; i < kHG; ++i) o[i] *= alpha[g][i];
+                                            tmem_st8(tmem + lane_off + col, o);
+                                        }
+                                    }
+                                tmem_wait_st();
+                            }
+                        }
+                        // weights, their three parts into shared memory (16 heads x 8
+                        // tokens core matrices; this group has 8 of the 16)
+#pragma unroll
+                        for (int g = 0; g < C::SBR; ++g) {
+                            uint32_t h[kHG / 2];
+#pragma unroll
+                            for (int i = 0; i < kHG; i += 2) {
+                                const float w0 = fast_exp2(z[g][i] - m[g][i]), w1 = fast_exp2(z[g][i + 1] - m[g][i + 1]);
+                                l[st * C::SBR + g][i] = fmaf(w0, rs[g], l[st * C::SBR + g][i]);
+                                l[st * C::SBR + g][i + 1] = fmaf(w1, rs[g], l[st * C::SBR + g][i + 1]);
+                                h[i / 2] = pack_half(w0, w1);
+                            }
+                            uint8_t* dst = sm + C::OFF_P + slot * C::P_BYTES + g * C::P_BRANCH_BYTES + (row >> 3) * 128 +
+                                           (row & 7) * 16 + sg * 8;
+#pragma unroll
+                            for (int part = 0; part < 3; ++part) {
+                                if (part > 0) {
+#pragma unroll
+                                    for (int i = 0; i < kHG / 2; ++i) {
+                                        h[i] = half_rest(h[i]);
+                                        if (part == 2) h[i] += 0x00800080u;  // the last part is rounded, not cut
+                                    }
+                                }
+                                *reinterpret_cast<uint2*>(dst + part * C::P_PART_BYTES) =
+                                    make_uint2(upper_bytes(h[0], h[1]), upper_bytes(h[2], h[3]));
+                            }
+                        }
+                        // rows past the end of the sequence become zero before the output MMA
+                        // reads them: this group clears its half of each row
+                        if (masked) {
+#pragma unroll
+                            for (int c = 0; c < C::CPS; ++c) {
+                                uint8_t* p = sm + C::OFF_CHUNK + ((gs * C::CPS + c) % C::NSTAGE) * C::CHUNK_BYTES + row * 128 + sg * 64;
+#pragma unroll
+                                for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(p + u * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            }
+                        }
+                        fence_proxy_async_smem();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&misc.p_full[slot]);
+                        ++gs;
+                    }
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) sig[b] = sig_next[b];
+                    ++tcnt;
+                }
+                if (dead) continue;
+
+                // ---------------------------------------------------- epilogue
+                constexpr int NV = NB * kHG;  // (branch, head) values of the group
+                {
+                    float f[NV];
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int i = 0; i < kHG; ++i) f[b * kHG + i] = l[b][i];
+                    warp_sum_scatter<NV, 16, NV>(f, lane);
+                    if constexpr (NV >= 32) {
+                        misc.red_sum[quad][NV * sg + lane] = f[0];
+                    } else {
+                        constexpr int SPAN = 32 / NV;
+                        if ((lane & (SPAN - 1)) == 0) misc.red_sum[quad][NV * sg + lane / SPAN] = f[0];
+                    }
+                }
+                bad = named_bar_or_id<128>(gbar, bad);  // also publishes red_sum
+                const bool single = cum >= A0 && cum + (tiles - 1) * kTileCost < A1;
+                const size_t slot = (size_t)grp.slot0 + grp.ci + n;
+                if (stid < NV) {
+                    const int c = NV * sg + stid;
+                    const float lt = misc.red_sum[0][c] + misc.red_sum[1][c] + misc.red_sum[2][c] + misc.red_sum[3][c];
+                    const int b = stid / kHG, i = hoff + stid % kHG;
+                    misc.inv_l[b * kHP + i] = 1.0f / lt;
+                    if (!single)
+                        a.lse_part[(slot * NB + b) * kHP + i] = bad ? bad_split_marker() : misc.m_run[b * kHP + i] + __log2f(lt);
+                }
+                {
+                    const bool ok = mbar_wait(&misc.p_empty[(gs - 1) % C::NSP], ((gs - 1) / C::NSP) & 1);
+                    if (named_bar_or_id<128>(gbar, !ok)) {
+                        dead = true;
+                        continue;
+                    }
+                }
+                tc_fence_after();
+                constexpr int WIDTH = DC >= 128 ? 128 : DC;  // valid rows of an output block
+#pragma unroll
+                for (int blk = 0; blk < C::O_BLOCKS; ++blk) {
+                    const int g2 = blk % C::BPC, gp = blk / C::BPC;
+                    const int first = g2 * WIDTH;
+                    const int b = (gp * 128 + first) / DC;
+                    const int k = (gp * 128 + first) % DC + (row - first);
+                    float o[kHG], o1[kHG], o2[kHG];
+                    tmem_ld8(tmem + lane_off + blk * kPN + hoff, o);
+                    tmem_ld8(tmem + lane_off + blk * kPN + kHP + hoff, o1);
+                    tmem_ld8(tmem + lane_off + blk * kPN + 2 * kHP + hoff, o2);
+                    tmem_wait_ld();
+                    if (row < first || row >= first + WIDTH) continue;
+                    const float* inv = &misc.inv_l[b * kHP + hoff];
+#pragma unroll
+                    for (int i = 0; i < kHG; ++i) o[i] = bad ? 0.f : (o[i] + (o1[i] + o2[i])) * inv[i];
+                    if (single) {
+                        __nv_bfloat16* dst = a.out + (((size_t)n * H + grp.h0 + hoff) * NB + b) * DC + k;
+#pragma unroll
+                        for (int i = 0; i < kHG; ++i)
+                            if (hoff + i < grp.hn) dst[(size_t)i * C::W] = to_bf16(o[i] * a.out_scale);
+                    } else {
+                        st_global_v8(a.o_part + ((slot * NB + b) * DC + k) * kHP + hoff, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
+                    }
+                }
+                if (bad && stid == 0) record_error(a.err, MLRA_ERR_DEVICE_BAD_INDEX);
+                tc_fence_before();
+                named_bar_sync_id<128>(gbar);  // inv_l and red_sum are reused by the next range
+                if (stid == 0) {
+                    if (!single) {
+                        if (pend_a < 0) pend_a = n; else pend_b = n;
+                    }
+                    if (sg == 0) {
+                        misc.last_seg[0] = n;
+                        misc.last_seg[1] = cum;
+                        misc.last_seg[2] = tiles;
+                        misc.last_seg[3] = c1_member;
+                    }
+                }
+            }
+            if (dead && stid == 0) {
+                record_error(a.err, MLRA_ERR_DEVICE_TIMEOUT);
+                *abort_flag = 1;
+            }
+            // both groups' partial stores, then one release fence, then the counts
+            const bool any_dead = named_bar_or<6, 256>(dead);
+            if (!any_dead && sg == 0 && stid == 0 && pend_a >= 0) {
+                fence_acq_rel_gpu();
+                red_add_relaxed_gpu(a.seq_cnt + grp.cnt0 + pend_a, 1);
+                if (pend_b >= 0) red_add_relaxed_gpu(a.seq_cnt + grp.cnt0 + pend_b, 1);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+    if (*abort_flag) return;
+    merge_tail<NB, DC, kHP>(a, grp, misc.last_seg[0], misc.last_seg[1], misc.last_seg[2], misc.last_seg[3] != 0, chunk,
+                            reinterpret_cast<float*>(sm + C::OFF_CHUNK), &misc.merge_flag, &misc.merge_full);
+}
+
+template <int NB, int DC, int DR>
+cudaError_t launch_cfg(const DecodeArgs& a, const float* latent_scale, cudaStream_t stream) {
+    using C = Cfg<NB, DC, DR>;
+    Maps maps;
+    const uint64_t rows = (uint64_t)a.num_pages * a.page_size;
+    if (!encode_rows(&maps.lat, a.latent, 1, C::W, rows, 128, a.page_size, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_rows(&maps.rope, a.rope, 2, DR, rows, DR, a.page_size, rope_swizzle(DR)))
+        return cudaErrorInvalidValue;
+    auto kernel = decode_fp8_kernel<NB, DC, DR>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    // the merge stages below MISC (the bound of decode_tc.cu)
+    for (int S = 2; S <= a.num_ctas; ++S) {
+        const size_t share = ((size_t)C::W + S - 2) / (S - 1);
+        if (sizeof(float) * ((size_t)S * NB * kHP + S * share * kHP) > (size_t)C::OFF_MISC) return cudaErrorInvalidConfiguration;
+    }
+    // cooperative: every CTA is resident, so the merge's waits end
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.num_ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, maps, a, latent_scale);
+}
+
+template <int NB, int DC>
+cudaError_t launch_shape(const DecodeArgs& a, const float* latent_scale, cudaStream_t stream) {
+    return a.d_r == 64 ? launch_cfg<NB, DC, 64>(a, latent_scale, stream) : launch_cfg<NB, DC, 32>(a, latent_scale, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_fp8(const DecodeArgs& a, const float* latent_scale, cudaStream_t stream) {
-    switch (a.d_c) {
-        case 64: return launch_dc<64>(a, latent_scale, stream);
-        case 128: return launch_dc<128>(a, latent_scale, stream);
-        case 256: return launch_dc<256>(a, latent_scale, stream);
-        case 512: return launch_dc<512>(a, latent_scale, stream);
-    }
+#define MLRA_FP8_CASE(NB_, DC_) \
+    if (a.branches == NB_ && a.d_c == DC_) return launch_shape<NB_, DC_>(a, latent_scale, stream);
+    MLRA_FP8_CASE(2, 64)
+    MLRA_FP8_CASE(4, 64)
+    MLRA_FP8_CASE(1, 128)
+    MLRA_FP8_CASE(2, 128)
+    MLRA_FP8_CASE(4, 128)
+    MLRA_FP8_CASE(1, 256)
+    MLRA_FP8_CASE(2, 256)
+    MLRA_FP8_CASE(1, 512)
+#undef MLRA_FP8_CASE
     return cudaErrorInvalidValue;
 }
 

@@ -192,7 +192,18 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint6
                  : "memory");
 }
 
-// The same with A in TMEM (128 lanes = rows, two bf16 values of K per column).
+// D[tmem] (+)= A[smem] * B[smem], kind::f8f6f4 (8-bit inputs, K = 32, fp32
+// accumulate).
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+                 ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+// kind::f16 with A in TMEM (128 lanes = rows, two bf16 values of K per column).
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                             uint32_t accumulate) {
     asm volatile("{\n\t.reg .pred p;\n\t"
@@ -334,6 +345,15 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint
 //   (1 = bf16), 15 A major (0 K, 1 MN), 16 B major, 17-22 N >> 3, 24-28 M >> 4.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) |
+           ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Instruction descriptor of kind::f8f6f4 with fp32 D: the A and B formats are
+// 0 for e4m3, 1 for e5m2; the other fields as above.
+enum : uint32_t { kE4M3 = 0, kE5M2 = 1 };
+__host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int N, uint32_t a_format, uint32_t b_format, bool a_mn_major,
+                                                    bool b_mn_major) {
+    return (1u << 4) | (a_format << 7) | (b_format << 10) | ((a_mn_major ? 1u : 0u) << 15) |
            ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 

@@ -27,8 +27,14 @@
 // rounded (a token row's sigma, its logarithm and reciprocal are per-thread
 // scalars).  Sums, references and outputs are fp32.
 //
-// A step of the MMA <-> softmax pipeline is two branches where a branch is at
-// most 128 wide (two per thread and barrier), else one.
+// A step of the MMA <-> softmax pipeline is two branches, one for each softmax
+// group of four warps (16 heads a thread), or the only branch with its heads
+// split between the groups.  The four warps of a group share a reference per
+// (branch, head), which a warp that meets a score past it has to raise; they
+// vote on that through an mbarrier: a warp casts its vote when it has its
+// scores, goes on as if nobody needed a raise, and looks at the votes before
+// it hands its weights over (by then all have voted, so nobody waits; a
+// barrier in this place cost a third of the step).
 #include <cuda_fp8.h>
 
 #include <cstddef>
@@ -43,7 +49,6 @@ namespace mlra {
 namespace {
 
 constexpr int kHP = 16;       // heads per tile
-constexpr int kHG = 8;        // heads per softmax warpgroup
 constexpr int kSN = 2 * kHP;  // score columns of a branch: hi and lo query parts
 constexpr int kPN = 3 * kHP;  // output columns of a block: three probability parts
 constexpr int kMaxStages = 16;
@@ -56,7 +61,9 @@ struct Cfg {
     static constexpr int W = NB * DC;                            // latent bytes per token
     static constexpr int NCH = W / 128;                          // 128-byte chunks of a token row
     static constexpr int BPC = DC >= 128 ? 1 : 128 / DC;         // branches per chunk
-    static constexpr int SBR = DC > 128 || NB == 1 ? 1 : 2;      // branches per step
+    static constexpr int SBR = NB == 1 ? 1 : 2;                  // branches per step
+    static constexpr bool BY_BRANCH = SBR == 2;                  // the softmax groups split a step by branch, else by heads
+    static constexpr int HG = BY_BRANCH ? 16 : 8;                // heads of a softmax thread
     static constexpr int CPS = SBR * DC / 128;                   // chunks per step
     static constexpr int NSTEP = NB / SBR;                       // steps per tile
     static constexpr int CHUNK_BYTES = kT * 128;
@@ -92,7 +99,7 @@ struct Cfg {
     static constexpr int COLS = R_COL0 + NRS * kHP;
     static constexpr int TMEM_COLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
     static_assert(NB % SBR == 0 && SBR * DC % 128 == 0 && NSTEP * CPS == NCH, "steps fill whole chunks");
-    static_assert(NSTAGE >= 2 * CPS && NROPE <= 4 && NSP <= 4, "rings");
+    static_assert(CPS >= 1 && NSTAGE >= 2 * CPS && NROPE <= 4 && NSP <= 4, "rings");
     static_assert(COLS <= 512 && SMEM_BYTES <= kSmemLimit, "TMEM and shared memory");
     static_assert(Q_BYTES % 1024 == 0 && ROPE_BYTES % 1024 == 0 && P_BYTES % 1024 == 0, "regions stay aligned");
 };
@@ -105,6 +112,7 @@ struct Misc {
     uint64_t s_full[4];   // step g in slot g % NSP: its scores are in TMEM
     uint64_t p_full[4];   // its probabilities are in shared memory
     uint64_t p_empty[4];  // its output MMA finished
+    uint64_t vote[2][4];  // softmax group, step: its four warps have voted
     uint64_t q_full;      // a range's queries are in shared memory (written by the softmax warps)
     uint64_t drain[2];
     uint64_t merge_full;
@@ -113,8 +121,9 @@ struct Misc {
     int plan[4];
     int last_seg[4];
     int merge_flag;
+    int raise[2][4];                  // some warp of the group needs a higher reference in this step
     float q_max[8];                   // largest query magnitude seen by each softmax warp
-    float red_max[4][2 * kHP];        // [quadrant][step branch, head]
+    float red_max[2][4][kHP];         // [group][quadrant][head]
     float red_sum[4][4 * kHP];        // [quadrant][group, branch, head]
     alignas(16) float m_run[4 * kHP]; // reference M per (branch, head)
     float inv_l[4 * kHP];
@@ -154,20 +163,6 @@ __device__ __forceinline__ uint32_t half_rest(uint32_t h) {
 // The upper bytes of four halves.
 __device__ __forceinline__ uint32_t upper_bytes(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7531); }
 
-// The scales of one token row, every branch (one 16-token block of its page).
-template <int NB>
-__device__ __forceinline__ void load_scales(const float* p, float (&s)[NB]) {
-    if constexpr (NB == 4) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(p));
-        s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
-    } else if constexpr (NB == 2) {
-        const float2 v = __ldg(reinterpret_cast<const float2*>(p));
-        s[0] = v.x, s[1] = v.y;
-    } else {
-        s[0] = __ldg(p);
-    }
-}
-
 template <int NB, int DC, int DR>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ DecodeArgs a,
@@ -189,6 +184,10 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
             mbar_init(&misc.s_full[i], 1);
             mbar_init(&misc.p_full[i], 8);
             mbar_init(&misc.p_empty[i], 1);
+            for (int g = 0; g < 2; ++g) {
+                mbar_init(&misc.vote[g][i], 4);
+                misc.raise[g][i] = 0;
+            }
         }
         mbar_init(&misc.q_full, 8);
         mbar_init(&misc.drain[0], 1);
@@ -361,8 +360,8 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                             // 32 bytes (K) at a time; the chunk's branch (or, of two, the one of its half)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk) {
-                                const int g = DC == 64 ? kk / 2 : DC == 128 ? c : 0;
-                                const bool first = DC == 64 ? kk % 2 == 0 : DC == 128 ? kk == 0 : (c | kk) == 0;
+                                const int g = DC == 64 ? kk / 2 : c * 128 / DC;
+                                const bool first = DC == 64 ? kk % 2 == 0 : c * 128 % DC == 0 && kk == 0;
                                 if (elect_one()) mma_f8(dS + g * kSN, a0 + kk * 2, q0 + kk * 2, ID_S, first ? 0u : 1u);
                             }
                             if (++stage == (uint32_t)C::NSTAGE) stage = 0, phase ^= 1;
@@ -412,7 +411,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                             for (int g2 = 0; g2 < C::BPC; ++g2) {
                                 // branch of the step whose P multiplies this chunk (the rows of a
                                 // shared chunk's other branch are left out later)
-                                const int g = DC == 64 ? g2 : DC == 128 ? c : 0;
+                                const int g = DC == 64 ? g2 : c * 128 / DC;
                                 const uint32_t d = tmem + ((st * C::CPS + c) * C::BPC + g2) * kPN;
 #pragma unroll
                                 for (int kt = 0; kt < kT / 32; ++kt)
@@ -441,8 +440,10 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
             __syncwarp();
         } else {
             // ------------------------------------------------------------ queries, softmax, epilogue
-            const int sg = warp >= 7;                        // softmax group: heads [8 sg, 8 sg + 8)
-            const int hoff = kHG * sg;
+            constexpr int HG = C::HG;
+            const int sg = warp >= 7;                        // softmax group
+            const int hoff = C::BY_BRANCH ? 0 : HG * sg;     // its first head
+            const int bsel = C::BY_BRANCH ? sg : 0;          // its branch of a step
             const uint32_t gbar = 3 + sg;                    // its named barrier (128 threads)
             const int quad = warp & 3;                       // TMEM lane quadrant
             const int row = quad * 32 + lane;                // token (S) / latent column (O)
@@ -450,7 +451,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
             const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
             const int H = a.heads;
             uint32_t gs = 0, tcnt = 0;
-            float l[NB][kHG];
+            float l[C::NSTEP][HG];  // this thread's share of sum w / sigma
             bool dead = false;
             int pend_a = -1, pend_b = -1;
 
@@ -544,112 +545,152 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                     }
                 }
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
+                for (int st = 0; st < C::NSTEP; ++st)
 #pragma unroll
-                    for (int i = 0; i < kHG; ++i) l[b][i] = 0.f;
+                    for (int i = 0; i < HG; ++i) l[st][i] = 0.f;
 
-                // this thread's token: its page one tile ahead, its scales with it
+                // this thread's token: its page two tiles ahead, the scales of its
+                // branches one tile ahead
                 auto page_of = [&](int j) { return j < te && j * kT + row < L ? __ldg(bt + (j * kT + row) / P) : 0; };
-                auto scales_of = [&](int page, int j, float (&s)[NB]) {
+                auto scales_of = [&](int page, int j, float (&s)[C::NSTEP]) {
                     const bool real = page >= 0 && page < a.num_pages;
-                    load_scales<NB>(latent_scale + ((size_t)(real ? page : 0) * P + (j * kT + row) % P) / kFp8Block * NB, s);
+                    const float* p = latent_scale + ((size_t)(real ? page : 0) * P + (j * kT + row) % P) / kFp8Block * NB + bsel;
+#pragma unroll
+                    for (int st = 0; st < C::NSTEP; ++st) s[st] = __ldg(p + st * C::SBR);
                     return real;
                 };
-                float sig[NB], sig_next[NB];
+                float sig[C::NSTEP], sig_next[C::NSTEP];
                 int page_next = page_of(tb + 1);
                 bad |= !scales_of(page_of(tb), tb, sig);
+                float r[HG];  // this token's RoPE score per head in log2 units
+
+                // weights of a step from its scores: z = log2 of p sigma
+                auto read_scores = [&](uint32_t slot, float k, float ls, bool masked, float (&z)[HG]) {
+                    float low[HG];
+                    const uint32_t at = tmem + lane_off + C::S_COL0 + slot * C::S_SLOT_COLS + bsel * kSN + hoff;
+                    tmem_ld_cols<HG>(at, z);
+                    tmem_ld_cols<HG>(at + kHP, low);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < HG; ++i) z[i] = fmaf(z[i] + low[i], k, r[i] + ls);
+                    if (masked) {
+#pragma unroll
+                        for (int i = 0; i < HG; ++i) z[i] = -INFINITY;
+                    }
+                };
+                // w = 2^z (z less its reference) and its three parts into shared
+                // memory (core matrices of 16 heads x 8 tokens)
+                auto write_weights = [&](uint32_t slot, float (&z)[HG]) {
+                    uint32_t h[HG / 2];
+#pragma unroll
+                    for (int i = 0; i < HG; i += 2) {
+                        z[i] = fast_exp2(z[i]);
+                        z[i + 1] = fast_exp2(z[i + 1]);
+                        h[i / 2] = pack_half(z[i], z[i + 1]);
+                    }
+                    uint8_t* dst = sm + C::OFF_P + slot * C::P_BYTES + bsel * C::P_BRANCH_BYTES + (row >> 3) * 128 + (row & 7) * 16 + hoff;
+#pragma unroll
+                    for (int part = 0; part < 3; ++part) {
+                        if (part > 0) {
+#pragma unroll
+                            for (int i = 0; i < HG / 2; ++i) {
+                                h[i] = half_rest(h[i]);
+                                if (part == 2) h[i] += 0x00800080u;  // the last part is rounded, not cut
+                            }
+                        }
+                        if constexpr (HG == 16)
+                            *reinterpret_cast<uint4*>(dst + part * C::P_PART_BYTES) =
+                                make_uint4(upper_bytes(h[0], h[1]), upper_bytes(h[2], h[3]), upper_bytes(h[4], h[5]), upper_bytes(h[6], h[7]));
+                        else
+                            *reinterpret_cast<uint2*>(dst + part * C::P_PART_BYTES) =
+                                make_uint2(upper_bytes(h[0], h[1]), upper_bytes(h[2], h[3]));
+                    }
+                };
 
                 for (int j = tb; j < te && !dead; ++j) {
                     const bool masked = j * kT + row >= L;
                     const int page_after = page_of(j + 2);
                     if (j + 1 < te) bad |= !scales_of(page_next, j + 1, sig_next);
                     page_next = page_after;
-                    float r[kHG];  // this token's RoPE score per head in log2 units
-#pragma unroll
+#pragma unroll 1
                     for (int st = 0; st < C::NSTEP; ++st) {
-                        const uint32_t slot = gs % C::NSP;
-                        const bool ok = mbar_wait(&misc.s_full[slot], (gs / C::NSP) & 1);
+                        const uint32_t slot = gs % C::NSP, parity = (gs / C::NSP) & 1;
+                        const float sigma = sig[0], ls = masked ? 0.f : fast_log2(sigma), k = sigma * alpha_q;
+                        const float rs = masked ? 0.f : __frcp_rn(sigma);
+                        float* m_step = &misc.m_run[(st * C::SBR + bsel) * kHP + hoff];
+                        float m[HG];
+                        auto load_m = [&]() {
+#pragma unroll
+                            for (int i = 0; i < HG; i += 4) {
+                                const float4 v = *reinterpret_cast<const float4*>(m_step + i);
+                                m[i] = v.x;
+                                m[i + 1] = v.y;
+                                m[i + 2] = v.z;
+                                m[i + 3] = v.w;
+                            }
+                        };
+                        load_m();
+                        const bool ok = mbar_wait(&misc.s_full[slot], parity);
                         tc_fence_after();
-                        float z[C::SBR][kHG], low[C::SBR][kHG];
-                        if (st == 0) tmem_ld8(tmem + lane_off + C::R_COL0 + (tcnt % C::NRS) * kHP + hoff, r);
-#pragma unroll
-                        for (int g = 0; g < C::SBR; ++g) {
-                            const uint32_t at = tmem + lane_off + C::S_COL0 + slot * C::S_SLOT_COLS + g * kSN + hoff;
-                            tmem_ld8(at, z[g]);
-                            tmem_ld8(at + kHP, low[g]);
-                        }
-                        tmem_wait_ld();
                         if (st == 0) {
+                            tmem_ld_cols<HG>(tmem + lane_off + C::R_COL0 + (tcnt % C::NRS) * kHP + hoff, r);
+                            tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < kHG; ++i) r[i] *= a.scale_log2;
+                            for (int i = 0; i < HG; ++i) r[i] *= a.scale_log2;
                         }
-                        float rs[C::SBR];  // 1 / sigma
-#pragma unroll
-                        for (int g = 0; g < C::SBR; ++g) {
-                            const float s = sig[st * C::SBR + g], ls = fast_log2(s), k = s * alpha_q;
-                            rs[g] = masked ? 0.f : __frcp_rn(s);
-#pragma unroll
-                            for (int i = 0; i < kHG; ++i)
-                                z[g][i] = masked ? -INFINITY : fmaf(z[g][i] + low[g][i], k, r[i] + ls);
-                        }
-                        float* m_step = &misc.m_run[st * C::SBR * kHP + hoff];  // [g * kHP + i]
+                        float z[HG];
+                        read_scores(slot, k, ls, masked, z);
                         if (j == tb) {
                             // the range's first token (always there) sets the references
                             if (stid == 0) {
 #pragma unroll
-                                for (int g = 0; g < C::SBR; ++g)
-#pragma unroll
-                                    for (int i = 0; i < kHG; ++i) m_step[g * kHP + i] = z[g][i] - kBase;
+                                for (int i = 0; i < HG; ++i) m_step[i] = z[i] - kBase;
                             }
                             named_bar_sync_id<128>(gbar);
+                            load_m();
                         }
-                        float m[C::SBR][kHG];
+                        float top = -INFINITY;
 #pragma unroll
-                        for (int g = 0; g < C::SBR; ++g)
-#pragma unroll
-                            for (int i = 0; i < kHG; i += 4) {
-                                const float4 v = *reinterpret_cast<const float4*>(m_step + g * kHP + i);
-                                m[g][i] = v.x;
-                                m[g][i + 1] = v.y;
-                                m[g][i + 2] = v.z;
-                                m[g][i + 3] = v.w;
-                            }
-                        bool need = false;
-#pragma unroll
-                        for (int g = 0; g < C::SBR; ++g)
-#pragma unroll
-                            for (int i = 0; i < kHG; ++i) need |= z[g][i] > m[g][i] + (kBase + kRescaleLog2);
-                        if (named_bar_or_id<128>(gbar, need || !ok)) {
-                            if (named_bar_or_id<128>(gbar, !ok)) {
+                        for (int i = 0; i < HG; ++i) {
+                            z[i] -= m[i];
+                            top = fmaxf(top, z[i]);
+                        }
+                        const bool need = __any_sync(0xffffffffu, top > kBase + kRescaleLog2 || !ok);
+                        if (lane == 0) {
+                            if (need) *reinterpret_cast<volatile int*>(&misc.raise[sg][slot]) = 1;
+                            mbar_arrive(&misc.vote[sg][slot]);
+                        }
+                        write_weights(slot, z);
+                        // (every warp votes: what it waits for before is bounded well below this)
+                        const bool ok1 = mbar_wait(&misc.vote[sg][slot], parity, 8000000000ull);
+                        if (!ok1 || *reinterpret_cast<volatile int*>(&misc.raise[sg][slot]) != 0) {
+                            // all four warps: exact column maxima, new references, O and l at
+                            // them, the weights again
+                            if (!ok1 || named_bar_or_id<128>(gbar, !ok)) {
                                 dead = true;
                                 break;
                             }
-                            // exact column maxima of the tile, new references, O and l at them
-#pragma unroll
-                            for (int g = 0; g < C::SBR; ++g) {
-                                const float v = warp_colmax8(z[g], lane);
-                                if ((lane & 3) == 0) misc.red_max[quad][g * kHP + hoff + lane / 4] = v;
-                            }
+                            read_scores(slot, k, ls, masked, z);
+                            constexpr int SPAN = 32 / HG;
+                            const float v = warp_colmax<HG>(z, lane);
+                            if ((lane & (SPAN - 1)) == 0) misc.red_max[sg][quad][lane / SPAN] = v;
                             named_bar_sync_id<128>(gbar);
-                            float alpha[C::SBR][kHG];
+                            float alpha[HG];
 #pragma unroll
-                            for (int g = 0; g < C::SBR; ++g)
-#pragma unroll
-                                for (int i = 0; i < kHG; ++i) {
-                                    const int c = g * kHP + hoff + i;
-                                    const float top = fmaxf(fmaxf(misc.red_max[0][c], misc.red_max[1][c]),
-                                                            fmaxf(misc.red_max[2][c], misc.red_max[3][c]));
-                                    const float mnew = fmaxf(m[g][i], top - kBase);
-                                    alpha[g][i] = fast_exp2(m[g][i] - mnew);
-                                    m[g][i] = mnew;
-                                    l[st * C::SBR + g][i] *= alpha[g][i];
-                                }
+                            for (int i = 0; i < HG; ++i) {
+                                const float t = fmaxf(fmaxf(misc.red_max[sg][0][i], misc.red_max[sg][1][i]),
+                                                      fmaxf(misc.red_max[sg][2][i], misc.red_max[sg][3][i]));
+                                const float mnew = fmaxf(m[i], t - kBase);
+                                alpha[i] = fast_exp2(m[i] - mnew);
+                                m[i] = mnew;
+                                l[0][i] *= alpha[i];
+                                z[i] -= mnew;
+                            }
                             // (everyone has read the old references before the barrier above)
                             if (stid == 0) {
 #pragma unroll
-                                for (int g = 0; g < C::SBR; ++g)
-#pragma unroll
-                                    for (int i = 0; i < kHG; ++i) m_step[g * kHP + i] = m[g][i];
+                                for (int i = 0; i < HG; ++i) m_step[i] = m[i];
+                                misc.raise[sg][slot] = 0;
                             }
                             named_bar_sync_id<128>(gbar);
                             if (j > tb) {
@@ -659,52 +700,24 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                                     break;
                                 }
                                 tc_fence_after();
+#pragma unroll 1
+                                for (int e = 0; e < C::CPS * C::BPC * 3; ++e) {
+                                    const int part = e % 3, c = e / 3 / C::BPC, g2 = e / 3 % C::BPC;
+                                    if (C::BY_BRANCH && (DC == 64 ? g2 : c * 128 / DC) != sg) continue;
+                                    const uint32_t at = tmem + lane_off + ((st * C::CPS + c) * C::BPC + g2) * kPN + part * kHP + hoff;
+                                    float o[HG];
+                                    tmem_ld_cols<HG>(at, o);
+                                    tmem_wait_ld();
 #pragma unroll
-                                for (int c = 0; c < C::CPS; ++c)
-#pragma unroll
-                                    for (int g2 = 0; g2 < C::BPC; ++g2) {
-                                        const int g = DC == 64 ? g2 : DC == 128 ? c : 0;
-#pragma unroll
-                                        for (int part = 0; part < 3; ++part) {
-                                            const uint32_t col = ((st * C::CPS + c) * C::BPC + g2) * kPN + part * kHP + hoff;
-                                            float o[kHG];
-                                            tmem_ld8(tmem + lane_off + col, o);
-                                            tmem_wait_ld();
-#pragma unroll
-                                            for (int i = 0; i < kHG; ++i) o[i] *= alpha[g][i];
-                                            tmem_st8(tmem + lane_off + col, o);
-                                        }
-                                    }
+                                    for (int i = 0; i < HG; ++i) o[i] *= alpha[i];
+                                    tmem_st_cols<HG>(at, o);
+                                }
                                 tmem_wait_st();
                             }
+                            write_weights(slot, z);
                         }
-                        // weights, their three parts into shared memory (16 heads x 8
-                        // tokens core matrices; this group has 8 of the 16)
 #pragma unroll
-                        for (int g = 0; g < C::SBR; ++g) {
-                            uint32_t h[kHG / 2];
-#pragma unroll
-                            for (int i = 0; i < kHG; i += 2) {
-                                const float w0 = fast_exp2(z[g][i] - m[g][i]), w1 = fast_exp2(z[g][i + 1] - m[g][i + 1]);
-                                l[st * C::SBR + g][i] = fmaf(w0, rs[g], l[st * C::SBR + g][i]);
-                                l[st * C::SBR + g][i + 1] = fmaf(w1, rs[g], l[st * C::SBR + g][i + 1]);
-                                h[i / 2] = pack_half(w0, w1);
-                            }
-                            uint8_t* dst = sm + C::OFF_P + slot * C::P_BYTES + g * C::P_BRANCH_BYTES + (row >> 3) * 128 +
-                                           (row & 7) * 16 + sg * 8;
-#pragma unroll
-                            for (int part = 0; part < 3; ++part) {
-                                if (part > 0) {
-#pragma unroll
-                                    for (int i = 0; i < kHG / 2; ++i) {
-                                        h[i] = half_rest(h[i]);
-                                        if (part == 2) h[i] += 0x00800080u;  // the last part is rounded, not cut
-                                    }
-                                }
-                                *reinterpret_cast<uint2*>(dst + part * C::P_PART_BYTES) =
-                                    make_uint2(upper_bytes(h[0], h[1]), upper_bytes(h[2], h[3]));
-                            }
-                        }
+                        for (int i = 0; i < HG; ++i) l[0][i] = fmaf(z[i], rs, l[0][i]);
                         // rows past the end of the sequence become zero before the output MMA
                         // reads them: this group clears its half of each row
                         if (masked) {
@@ -719,29 +732,38 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&misc.p_full[slot]);
+                        // the next step's branch first (the step loop is not unrolled: its code
+                        // has to stay in the instruction cache)
+                        if constexpr (C::NSTEP == 2) {
+#pragma unroll
+                            for (int i = 0; i < HG; ++i) {
+                                const float t = l[0][i];
+                                l[0][i] = l[1][i];
+                                l[1][i] = t;
+                            }
+                            const float t = sig[0];
+                            sig[0] = sig[1];
+                            sig[1] = t;
+                        }
                         ++gs;
                     }
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) sig[b] = sig_next[b];
+                    for (int st = 0; st < C::NSTEP; ++st) sig[st] = sig_next[st];
                     ++tcnt;
                 }
                 if (dead) continue;
 
                 // ---------------------------------------------------- epilogue
-                constexpr int NV = NB * kHG;  // (branch, head) values of the group
+                constexpr int NV = C::NSTEP * HG;  // (branch, head) values of the group
                 {
                     float f[NV];
 #pragma unroll
-                    for (int b = 0; b < NB; ++b)
+                    for (int st = 0; st < C::NSTEP; ++st)
 #pragma unroll
-                        for (int i = 0; i < kHG; ++i) f[b * kHG + i] = l[b][i];
+                        for (int i = 0; i < HG; ++i) f[st * HG + i] = l[st][i];
                     warp_sum_scatter<NV, 16, NV>(f, lane);
-                    if constexpr (NV >= 32) {
-                        misc.red_sum[quad][NV * sg + lane] = f[0];
-                    } else {
-                        constexpr int SPAN = 32 / NV;
-                        if ((lane & (SPAN - 1)) == 0) misc.red_sum[quad][NV * sg + lane / SPAN] = f[0];
-                    }
+                    constexpr int SPAN = 32 / NV;
+                    if ((lane & (SPAN - 1)) == 0) misc.red_sum[quad][NV * sg + lane / SPAN] = f[0];
                 }
                 bad = named_bar_or_id<128>(gbar, bad);  // also publishes red_sum
                 const bool single = cum >= A0 && cum + (tiles - 1) * kTileCost < A1;
@@ -749,7 +771,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                 if (stid < NV) {
                     const int c = NV * sg + stid;
                     const float lt = misc.red_sum[0][c] + misc.red_sum[1][c] + misc.red_sum[2][c] + misc.red_sum[3][c];
-                    const int b = stid / kHG, i = hoff + stid % kHG;
+                    const int b = stid / HG * C::SBR + bsel, i = hoff + stid % HG;
                     misc.inv_l[b * kHP + i] = 1.0f / lt;
                     if (!single)
                         a.lse_part[(slot * NB + b) * kHP + i] = bad ? bad_split_marker() : misc.m_run[b * kHP + i] + __log2f(lt);
@@ -769,22 +791,26 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                     const int first = g2 * WIDTH;
                     const int b = (gp * 128 + first) / DC;
                     const int k = (gp * 128 + first) % DC + (row - first);
-                    float o[kHG], o1[kHG], o2[kHG];
-                    tmem_ld8(tmem + lane_off + blk * kPN + hoff, o);
-                    tmem_ld8(tmem + lane_off + blk * kPN + kHP + hoff, o1);
-                    tmem_ld8(tmem + lane_off + blk * kPN + 2 * kHP + hoff, o2);
+                    if (C::BY_BRANCH && b % C::SBR != sg) continue;
+                    float o[HG], o1[HG], o2[HG];
+                    tmem_ld_cols<HG>(tmem + lane_off + blk * kPN + hoff, o);
+                    tmem_ld_cols<HG>(tmem + lane_off + blk * kPN + kHP + hoff, o1);
+                    tmem_ld_cols<HG>(tmem + lane_off + blk * kPN + 2 * kHP + hoff, o2);
                     tmem_wait_ld();
                     if (row < first || row >= first + WIDTH) continue;
                     const float* inv = &misc.inv_l[b * kHP + hoff];
 #pragma unroll
-                    for (int i = 0; i < kHG; ++i) o[i] = bad ? 0.f : (o[i] + (o1[i] + o2[i])) * inv[i];
+                    for (int i = 0; i < HG; ++i) o[i] = bad ? 0.f : (o[i] + (o1[i] + o2[i])) * inv[i];
                     if (single) {
                         __nv_bfloat16* dst = a.out + (((size_t)n * H + grp.h0 + hoff) * NB + b) * DC + k;
 #pragma unroll
-                        for (int i = 0; i < kHG; ++i)
+                        for (int i = 0; i < HG; ++i)
                             if (hoff + i < grp.hn) dst[(size_t)i * C::W] = to_bf16(o[i] * a.out_scale);
                     } else {
-                        st_global_v8(a.o_part + ((slot * NB + b) * DC + k) * kHP + hoff, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
+                        float* dst = a.o_part + ((slot * NB + b) * DC + k) * kHP + hoff;
+#pragma unroll
+                        for (int i = 0; i < HG; i += 8)
+                            st_global_v8(dst + i, o[i], o[i + 1], o[i + 2], o[i + 3], o[i + 4], o[i + 5], o[i + 6], o[i + 7]);
                     }
                 }
                 if (bad && stid == 0) record_error(a.err, MLRA_ERR_DEVICE_BAD_INDEX);

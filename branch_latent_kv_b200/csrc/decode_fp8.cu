@@ -2,8 +2,10 @@
 // cores (mlra_decode_fp8): mlra_decode with c_b[t] = sigma_b[t / 16] e_b[t],
 // e an e4m3 value.
 //
-// The roles, the split plan and the merge are those of decode_tc.cu (same
-// warps, one persistent CTA per SM); what the 8-bit cache changes:
+// The split plan, the merge and the pipeline are those of decode_tc.cu: one
+// persistent CTA per SM walks its tiles of 128 tokens; warp 0 copies, warp 1
+// issues the score MMAs, warp 2 the output MMAs.  What the 8-bit cache
+// changes:
 //
 // The latents go to the tensor cores as they lie in memory (kind::f8f6f4),
 // so a token costs half the shared-memory reads that bound the MMAs here
@@ -27,14 +29,16 @@
 // rounded (a token row's sigma, its logarithm and reciprocal are per-thread
 // scalars).  Sums, references and outputs are fp32.
 //
-// A step of the MMA <-> softmax pipeline is two branches, one for each softmax
-// group of four warps (16 heads a thread), or the only branch with its heads
-// split between the groups.  The four warps of a group share a reference per
-// (branch, head), which a warp that meets a score past it has to raise; they
-// vote on that through an mbarrier: a warp casts its vote when it has its
-// scores, goes on as if nobody needed a raise, and looks at the votes before
-// it hands its weights over (by then all have voted, so nobody waits; a
-// barrier in this place cost a third of the step).
+// Softmax: four groups of four warps, each the owner of one branch's 16 heads
+// (of half of them with two branches, a quarter with one), a thread having
+// one token of the tile.  With half the bytes a tile lasts 1.9 us at HBM's
+// rate, less than one group takes for two branches (2.1 us, the two-group
+// layout of decode_tc.cu), so the branches are worked on side by side.
+// The four warps of a group share the reference M of each head, which a warp
+// that meets a score past it has to raise; they vote on that through an
+// mbarrier: a warp casts its vote when it has its scores, goes on as if nobody
+// needed a raise, and looks at the votes before it hands its weights over (a
+// barrier in this place cost a quarter of the step).
 #include <cuda_fp8.h>
 
 #include <cstddef>
@@ -55,6 +59,9 @@ constexpr int kMaxStages = 16;
 // the reference M sits 2^kBase below the largest weight when it is set, and a
 // weight may pass that by 2^kRescaleLog2: at most 2^15, e5m2 holds 1.75 2^15
 constexpr float kBase = 7.0f;
+constexpr int kGroups = 4;                      // softmax groups of four warps
+constexpr int kSoft = kGroups * 128;            // softmax threads
+constexpr int kFp8Threads = 128 + kSoft;        // and the copy, MMA and helper warps
 
 template <int NB, int DC, int DR>
 struct Cfg {
@@ -62,8 +69,9 @@ struct Cfg {
     static constexpr int NCH = W / 128;                          // 128-byte chunks of a token row
     static constexpr int BPC = DC >= 128 ? 1 : 128 / DC;         // branches per chunk
     static constexpr int SBR = NB == 1 ? 1 : 2;                  // branches per step
-    static constexpr bool BY_BRANCH = SBR == 2;                  // the softmax groups split a step by branch, else by heads
-    static constexpr int HG = BY_BRANCH ? 16 : 8;                // heads of a softmax thread
+    static constexpr int HG = kHP * NB / kGroups;                // heads of a softmax group: 16, 8 or 4
+    static constexpr int GPB = kGroups / NB;                     // groups per branch
+    static constexpr int GPS = GPB * SBR;                        // groups per step
     static constexpr int CPS = SBR * DC / 128;                   // chunks per step
     static constexpr int NSTEP = NB / SBR;                       // steps per tile
     static constexpr int CHUNK_BYTES = kT * 128;
@@ -98,6 +106,7 @@ struct Cfg {
     static constexpr int R_COL0 = S_COL0 + NSP * S_SLOT_COLS;
     static constexpr int COLS = R_COL0 + NRS * kHP;
     static constexpr int TMEM_COLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+    static_assert(NRS * NSTEP >= NSP + NSTEP - 1, "a RoPE score is read before its slot is written again");
     static_assert(NB % SBR == 0 && SBR * DC % 128 == 0 && NSTEP * CPS == NCH, "steps fill whole chunks");
     static_assert(CPS >= 1 && NSTAGE >= 2 * CPS && NROPE <= 4 && NSP <= 4, "rings");
     static_assert(COLS <= 512 && SMEM_BYTES <= kSmemLimit, "TMEM and shared memory");
@@ -112,7 +121,7 @@ struct Misc {
     uint64_t s_full[4];   // step g in slot g % NSP: its scores are in TMEM
     uint64_t p_full[4];   // its probabilities are in shared memory
     uint64_t p_empty[4];  // its output MMA finished
-    uint64_t vote[2][4];  // softmax group, step: its four warps have voted
+    uint64_t vote[kGroups];  // a group's four warps have voted on a tile
     uint64_t q_full;      // a range's queries are in shared memory (written by the softmax warps)
     uint64_t drain[2];
     uint64_t merge_full;
@@ -121,14 +130,15 @@ struct Misc {
     int plan[4];
     int last_seg[4];
     int merge_flag;
-    int raise[2][4];                  // some warp of the group needs a higher reference in this step
-    float q_max[8];                   // largest query magnitude seen by each softmax warp
-    float red_max[2][4][kHP];         // [group][quadrant][head]
-    float red_sum[4][4 * kHP];        // [quadrant][group, branch, head]
-    alignas(16) float m_run[4 * kHP]; // reference M per (branch, head)
-    float inv_l[4 * kHP];
+    int raise[kGroups][2];    // tile t (t & 1): some warp of the group needs a higher reference
+    float q_max[4 * kGroups]; // largest query magnitude seen by each softmax warp
+    float red_max[kGroups][4][kHP];  // [group][quadrant][head]
+    float red_sum[kGroups][4][kHP];
+    float inv_l[kGroups][kHP];
+    alignas(16) float m_run[kGroups][kHP];  // references M; read as float4
+    alignas(16) float alpha[kGroups][kHP];  // a raise: what O and l shrink by
 };
-static_assert(offsetof(Misc, m_run) % 16 == 0, "float4 access to m_run");
+static_assert(offsetof(Misc, m_run) % 16 == 0 && offsetof(Misc, alpha) % 16 == 0, "float4 access");
 
 struct Maps {
     CUtensorMap lat;   // latent bytes [pages * P][W]
@@ -164,7 +174,7 @@ __device__ __forceinline__ uint32_t half_rest(uint32_t h) {
 __device__ __forceinline__ uint32_t upper_bytes(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7531); }
 
 template <int NB, int DC, int DR>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kFp8Threads, 1)
 decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ DecodeArgs a,
                   const float* __restrict__ latent_scale) {
     using C = Cfg<NB, DC, DR>;
@@ -182,14 +192,14 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
         for (int i = 0; i < C::NROPE; ++i) mbar_init(&misc.rope_full[i], 1), mbar_init(&misc.rope_empty[i], 1);
         for (int i = 0; i < C::NSP; ++i) {
             mbar_init(&misc.s_full[i], 1);
-            mbar_init(&misc.p_full[i], 8);
+            mbar_init(&misc.p_full[i], 4 * C::GPS);
             mbar_init(&misc.p_empty[i], 1);
-            for (int g = 0; g < 2; ++g) {
-                mbar_init(&misc.vote[g][i], 4);
-                misc.raise[g][i] = 0;
-            }
         }
-        mbar_init(&misc.q_full, 8);
+        for (int g = 0; g < kGroups; ++g) {
+            mbar_init(&misc.vote[g], 4);
+            misc.raise[g][0] = misc.raise[g][1] = 0;
+        }
+        mbar_init(&misc.q_full, 4 * kGroups);
         mbar_init(&misc.drain[0], 1);
         mbar_init(&misc.drain[1], 1);
         mbar_init(&misc.merge_full, 1);
@@ -215,19 +225,19 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
             misc.plan[3] = cum_first;
         }
         __syncwarp();
-        named_bar_arrive<2, kThreads>();
+        named_bar_arrive<2, kFp8Threads>();
     } else {
         if (warp == 1) {
             tmem_alloc(&misc.tmem_base, C::TMEM_COLS);
             tmem_relinquish();
         }
         tc_fence_before();
-        named_bar_sync<2, kThreads>();
+        named_bar_sync<2, kFp8Threads>();
         tc_fence_after();
         wait_prerequisite_grid();
         n_first = misc.plan[2];
         cum_first = misc.plan[3];
-        if (warp == 6) {
+        if (warp == 3) {
             // sequences with an invalid length: zeros and an error code
             for (int m = blockIdx.x; m < a.batch; m += a.num_ctas) {
                 if (seq_tiles(__ldg(a.seqlens + m), P, a.max_pages) > 0) continue;
@@ -385,7 +395,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
             __syncwarp();
             mbar_wait(&misc.drain[0], 0, 200000000ull);
             __syncwarp();
-        } else if (warp == 6) {
+        } else if (warp == 2) {
             // ------------------------------------------------------------ output MMAs
             constexpr uint32_t ID_O = idesc_f8_f32(128, kPN, kE4M3, kE5M2, true, true);
             const uint32_t base = smem_u32(sm);
@@ -438,51 +448,48 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
             __syncwarp();
             mbar_wait(&misc.drain[1], 0, 200000000ull);
             __syncwarp();
-        } else {
+        } else if (warp >= 4) {
             // ------------------------------------------------------------ queries, softmax, epilogue
             constexpr int HG = C::HG;
-            const int sg = warp >= 7;                        // softmax group
-            const int hoff = C::BY_BRANCH ? 0 : HG * sg;     // its first head
-            const int bsel = C::BY_BRANCH ? sg : 0;          // its branch of a step
-            const uint32_t gbar = 3 + sg;                    // its named barrier (128 threads)
+            const int sg = (warp - 4) >> 2;                  // softmax group
+            const int br = sg / C::GPB;                      // its branch
+            const int hoff = HG * (sg % C::GPB);             // its first head
+            const int st = br / C::SBR, bsel = br % C::SBR;  // the branch's step in a tile, its place in the step
+            const uint32_t gbar = 8 + sg;                    // its named barrier (128 threads)
             const int quad = warp & 3;                       // TMEM lane quadrant
-            const int row = quad * 32 + lane;                // token (S) / latent column (O)
-            const int stid = (warp - (sg ? 7 : 2)) * 32 + lane;
-            const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-            const int H = a.heads;
-            uint32_t gs = 0, tcnt = 0;
-            float l[C::NSTEP][HG];  // this thread's share of sum w / sigma
+            const int row = quad * 32 + lane;                // token (S) / latent column (O); also the thread's number in the group
+            const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+            const int H = a.heads, log_p = __ffs(P) - 1;     // (P is a power of two)
+            uint32_t tcnt = 0;
             bool dead = false;
             int pend_a = -1, pend_b = -1;
 
-            // (both groups walk every range, so that they meet at the barrier
-            // below even when one has given up; then both stop)
+            // (all groups walk every range, so that they meet at the barrier
+            // below even when one has given up; then all stop)
             for (; next_segment(a, n, cum, A0, A1, L, tiles, tb, te, next_len); finish_segment(n, cum, tiles)) {
                 // ---------------------------------------------------- queries
-                // (the range before has no score MMA left: this thread has seen
-                // its last scores).  16 head rows; heads past the last are zero.
+                // (the range before has no score MMA left: its last step's
+                // probabilities are written).  16 head rows; heads past the last
+                // are zero.
                 float alpha_q;  // a score of the MMA times this is in log2 units (without sigma)
                 {
                     constexpr int UPR = C::W / 8;               // 8-value units per head row
-                    constexpr int U = kHP * UPR / 256 > 0 ? kHP * UPR / 256 : 1;
-                    const int sid = sg * 128 + stid;
+                    constexpr int UNITS = kHP * UPR;
+                    constexpr int U = (UNITS + kSoft - 1) / kSoft;
+                    const int sid = threadIdx.x - 128;
                     const __nv_bfloat16* q = a.q_lat + ((size_t)n * H + grp.h0) * C::W;
                     uint4 v[U];
                     uint32_t mx = 0;
 #pragma unroll
                     for (int i = 0; i < U; ++i) {
-                        const int u = sid + 256 * i;
-                        v[i] = u / UPR < grp.hn ? __ldg(reinterpret_cast<const uint4*>(q + (size_t)(u / UPR) * C::W) + u % UPR)
-                                                : make_uint4(0u, 0u, 0u, 0u);
+                        const int u = sid + kSoft * i;
+                        v[i] = u < UNITS && u / UPR < grp.hn ? __ldg(reinterpret_cast<const uint4*>(q + (size_t)(u / UPR) * C::W) + u % UPR)
+                                                             : make_uint4(0u, 0u, 0u, 0u);
                     }
                     constexpr int RU = DR / 8;                  // 16-byte units of a RoPE row
-                    if (sid < kHP * RU) {
-                        const int h = sid / RU, u = sid % RU;
-                        const uint4 w = h < grp.hn ? __ldg(reinterpret_cast<const uint4*>(a.q_rope + ((size_t)n * H + grp.h0 + h) * DR) + u)
-                                                   : make_uint4(0u, 0u, 0u, 0u);
-                        const int at = DR == 64 ? h * 128 + ((u ^ (h & 7)) << 4) : h * 64 + ((u ^ ((h >> 1) & 3)) << 4);
-                        *reinterpret_cast<uint4*>(sm + C::OFF_QR + at) = w;
-                    }
+                    uint4 rv = make_uint4(0u, 0u, 0u, 0u);
+                    if (sid < kHP * RU && sid / RU < grp.hn)
+                        rv = __ldg(reinterpret_cast<const uint4*>(a.q_rope + ((size_t)n * H + grp.h0 + sid / RU) * DR) + sid % RU);
 #pragma unroll
                     for (int i = 0; i < U; ++i) {
                         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -494,23 +501,27 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                         }
                     }
                     mx = __reduce_max_sync(0xffffffffu, mx);
-                    if (lane == 0) misc.q_max[sg * 4 + (warp - (sg ? 7 : 2))] = __uint_as_float(mx << 16);
-                    if (named_bar_or<5, 256>(dead)) {
+                    if (lane == 0) misc.q_max[warp - 4] = __uint_as_float(mx << 16);
+                    if (named_bar_or<5, kSoft>(dead)) {
                         dead = true;
                         break;
                     }
                     float top = misc.q_max[0];
 #pragma unroll
-                    for (int i = 1; i < 8; ++i) top = fmaxf(top, misc.q_max[i]);
+                    for (int i = 1; i < 4 * kGroups; ++i) top = fmaxf(top, misc.q_max[i]);
                     // the smallest power of two tau with top <= 448 tau (2^-100 at least: both it
                     // and its reciprocal are normal numbers)
                     const uint32_t tb32 = __float_as_uint(top);
                     const int e = max((int)(tb32 >> 23) - 135 + ((tb32 & 0x7fffffu) > 0x600000u), -100);
                     const float inv_tau = __uint_as_float((uint32_t)(127 - e) << 23);
                     alpha_q = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+                    if (sid < kHP * RU) {
+                        const int h = sid / RU, u = sid % RU;
+                        *reinterpret_cast<uint4*>(sm + C::OFF_QR + (DR == 64 ? h * 128 + ((u ^ (h & 7)) << 4) : h * 64 + ((u ^ ((h >> 1) & 3)) << 4))) = rv;
+                    }
 #pragma unroll
                     for (int i = 0; i < U; ++i) {
-                        const int u = sid + 256 * i, h = u / UPR, col = u % UPR * 8;
+                        const int u = sid + kSoft * i, h = u / UPR, col = u % UPR * 8;
                         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
                         uint32_t hi[4], lo[4];
 #pragma unroll
@@ -522,7 +533,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                             const float2 f = from_e4m3x2(hi[k]);
                             lo[k] = e4m3x2(x - f.x, y - f.y);
                         }
-                        if (U * 256 == kHP * UPR || u < kHP * UPR) {
+                        if (u < UNITS) {
                             uint8_t* dst = sm + C::OFF_Q + col / 128 * C::Q_CHUNK_BYTES + h * 128 +
                                            (((col % 128 / 16) ^ (h & 7)) << 4) + col % 16;
                             *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
@@ -536,7 +547,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                 bool bad = false;
                 const int32_t* bt = a.block_table + (size_t)n * a.max_pages;
                 int c1_member = 1;  // as in decode_tc.cu: whether the owner of the last tile merges
-                if (sg == 0 && stid == 0) {
+                if (threadIdx.x == 128) {
                     const int c1 = (cum + (tiles - 1) * kTileCost) / chunk;
                     for (int m = n + 1; m < a.batch; ++m) {
                         if (seq_tiles(__ldg(a.seqlens + m), a.page_size, a.max_pages) == 0) continue;
@@ -544,240 +555,207 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                         break;
                     }
                 }
-#pragma unroll
-                for (int st = 0; st < C::NSTEP; ++st)
-#pragma unroll
-                    for (int i = 0; i < HG; ++i) l[st][i] = 0.f;
 
-                // this thread's token: its page two tiles ahead, the scales of its
-                // branches one tile ahead
-                auto page_of = [&](int j) { return j < te && j * kT + row < L ? __ldg(bt + (j * kT + row) / P) : 0; };
-                auto scales_of = [&](int page, int j, float (&s)[C::NSTEP]) {
+                // this thread's token: its page two tiles ahead, its scale one
+                auto page_of = [&](int j) { return j < te && j * kT + row < L ? __ldg(bt + ((j * kT + row) >> log_p)) : 0; };
+                auto scale_of = [&](int page, int j) {
                     const bool real = page >= 0 && page < a.num_pages;
-                    const float* p = latent_scale + ((size_t)(real ? page : 0) * P + (j * kT + row) % P) / kFp8Block * NB + bsel;
-#pragma unroll
-                    for (int st = 0; st < C::NSTEP; ++st) s[st] = __ldg(p + st * C::SBR);
-                    return real;
+                    bad |= !real;
+                    return __ldg(latent_scale + (((size_t)(real ? page : 0) << log_p) + ((j * kT + row) & (P - 1))) / kFp8Block * NB + br);
                 };
-                float sig[C::NSTEP], sig_next[C::NSTEP];
                 int page_next = page_of(tb + 1);
-                bad |= !scales_of(page_of(tb), tb, sig);
-                float r[HG];  // this token's RoPE score per head in log2 units
+                float sig = scale_of(page_of(tb), tb), sig_next = 0.f;
+                float l[HG];  // this thread's share of sum w / sigma
+#pragma unroll
+                for (int i = 0; i < HG; ++i) l[i] = 0.f;
 
-                // weights of a step from its scores: z = log2 of p sigma
-                auto read_scores = [&](uint32_t slot, float k, float ls, bool masked, float (&z)[HG]) {
-                    float low[HG];
-                    const uint32_t at = tmem + lane_off + C::S_COL0 + slot * C::S_SLOT_COLS + bsel * kSN + hoff;
-                    tmem_ld_cols<HG>(at, z);
-                    tmem_ld_cols<HG>(at + kHP, low);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < HG; ++i) z[i] = fmaf(z[i] + low[i], k, r[i] + ls);
-                    if (masked) {
-#pragma unroll
-                        for (int i = 0; i < HG; ++i) z[i] = -INFINITY;
-                    }
-                };
-                // w = 2^z (z less its reference) and its three parts into shared
-                // memory (core matrices of 16 heads x 8 tokens)
-                auto write_weights = [&](uint32_t slot, float (&z)[HG]) {
-                    uint32_t h[HG / 2];
-#pragma unroll
-                    for (int i = 0; i < HG; i += 2) {
-                        z[i] = fast_exp2(z[i]);
-                        z[i + 1] = fast_exp2(z[i + 1]);
-                        h[i / 2] = pack_half(z[i], z[i + 1]);
-                    }
-                    uint8_t* dst = sm + C::OFF_P + slot * C::P_BYTES + bsel * C::P_BRANCH_BYTES + (row >> 3) * 128 + (row & 7) * 16 + hoff;
-#pragma unroll
-                    for (int part = 0; part < 3; ++part) {
-                        if (part > 0) {
-#pragma unroll
-                            for (int i = 0; i < HG / 2; ++i) {
-                                h[i] = half_rest(h[i]);
-                                if (part == 2) h[i] += 0x00800080u;  // the last part is rounded, not cut
-                            }
-                        }
-                        if constexpr (HG == 16)
-                            *reinterpret_cast<uint4*>(dst + part * C::P_PART_BYTES) =
-                                make_uint4(upper_bytes(h[0], h[1]), upper_bytes(h[2], h[3]), upper_bytes(h[4], h[5]), upper_bytes(h[6], h[7]));
-                        else
-                            *reinterpret_cast<uint2*>(dst + part * C::P_PART_BYTES) =
-                                make_uint2(upper_bytes(h[0], h[1]), upper_bytes(h[2], h[3]));
-                    }
-                };
-
-                for (int j = tb; j < te && !dead; ++j) {
+                for (int j = tb; j < te && !dead; ++j, ++tcnt) {
+                    const uint32_t gs = tcnt * C::NSTEP + st, slot = gs % C::NSP, parity = (gs / C::NSP) & 1;
                     const bool masked = j * kT + row >= L;
                     const int page_after = page_of(j + 2);
-                    if (j + 1 < te) bad |= !scales_of(page_next, j + 1, sig_next);
+                    if (j + 1 < te) sig_next = scale_of(page_next, j + 1);
                     page_next = page_after;
-#pragma unroll 1
-                    for (int st = 0; st < C::NSTEP; ++st) {
-                        const uint32_t slot = gs % C::NSP, parity = (gs / C::NSP) & 1;
-                        const float sigma = sig[0], ls = masked ? 0.f : fast_log2(sigma), k = sigma * alpha_q;
-                        const float rs = masked ? 0.f : __frcp_rn(sigma);
-                        float* m_step = &misc.m_run[(st * C::SBR + bsel) * kHP + hoff];
-                        float m[HG];
-                        auto load_m = [&]() {
+                    const float ls = fast_log2(sig), k = sig * alpha_q;
+                    const float rs = masked ? 0.f : __frcp_rn(sig);
+                    // z: log2 of p sigma per head
+                    float z[HG];
+                    auto read_scores = [&]() {
+                        constexpr int N = HG < 8 ? HG : 8;  // heads at a time (registers)
+                        const uint32_t s_at = lanes + C::S_COL0 + slot * C::S_SLOT_COLS + bsel * kSN + hoff;
+                        const uint32_t r_at = lanes + C::R_COL0 + (tcnt % C::NRS) * kHP + hoff;
 #pragma unroll
-                            for (int i = 0; i < HG; i += 4) {
-                                const float4 v = *reinterpret_cast<const float4*>(m_step + i);
-                                m[i] = v.x;
-                                m[i + 1] = v.y;
-                                m[i + 2] = v.z;
-                                m[i + 3] = v.w;
-                            }
-                        };
-                        load_m();
-                        const bool ok = mbar_wait(&misc.s_full[slot], parity);
-                        tc_fence_after();
-                        if (st == 0) {
-                            tmem_ld_cols<HG>(tmem + lane_off + C::R_COL0 + (tcnt % C::NRS) * kHP + hoff, r);
+                        for (int i0 = 0; i0 < HG; i0 += N) {
+                            float hi[N], low[N], r[N];
+                            tmem_ld_cols<N>(r_at + i0, r);
+                            tmem_ld_cols<N>(s_at + i0, hi);
+                            tmem_ld_cols<N>(s_at + kHP + i0, low);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < HG; ++i) r[i] *= a.scale_log2;
+                            for (int i = 0; i < N; ++i) z[i0 + i] = fmaf(hi[i] + low[i], k, fmaf(r[i], a.scale_log2, ls));
                         }
-                        float z[HG];
-                        read_scores(slot, k, ls, masked, z);
-                        if (j == tb) {
-                            // the range's first token (always there) sets the references
-                            if (stid == 0) {
+                        if (masked) {
 #pragma unroll
-                                for (int i = 0; i < HG; ++i) m_step[i] = z[i] - kBase;
+                            for (int i = 0; i < HG; ++i) z[i] = -INFINITY;
+                        }
+                    };
+                    auto less_references = [&]() {
+#pragma unroll
+                        for (int i = 0; i < HG; i += 4) {
+                            const float4 m = *reinterpret_cast<const float4*>(&misc.m_run[sg][i]);
+                            z[i] -= m.x;
+                            z[i + 1] -= m.y;
+                            z[i + 2] -= m.z;
+                            z[i + 3] -= m.w;
+                        }
+                    };
+                    // w = 2^z (z less its reference) and its three parts into shared
+                    // memory (core matrices of 16 heads x 8 tokens)
+                    auto write_weights = [&]() {
+                        uint32_t h[HG / 2];
+#pragma unroll
+                        for (int i = 0; i < HG; i += 2) {
+                            z[i] = fast_exp2(z[i]);
+                            z[i + 1] = fast_exp2(z[i + 1]);
+                            h[i / 2] = pack_half(z[i], z[i + 1]);
+                        }
+                        uint8_t* dst = sm + C::OFF_P + slot * C::P_BYTES + bsel * C::P_BRANCH_BYTES + (row >> 3) * 128 + (row & 7) * 16 + hoff;
+#pragma unroll
+                        for (int part = 0; part < 3; ++part) {
+                            if (part > 0) {
+#pragma unroll
+                                for (int i = 0; i < HG / 2; ++i) {
+                                    h[i] = half_rest(h[i]);
+                                    if (part == 2) h[i] += 0x00800080u;  // the last part is rounded, not cut
+                                }
                             }
-                            named_bar_sync_id<128>(gbar);
-                            load_m();
+                            if constexpr (HG == 16)
+                                *reinterpret_cast<uint4*>(dst + part * C::P_PART_BYTES) =
+                                    make_uint4(upper_bytes(h[0], h[1]), upper_bytes(h[2], h[3]), upper_bytes(h[4], h[5]), upper_bytes(h[6], h[7]));
+                            else if constexpr (HG == 8)
+                                *reinterpret_cast<uint2*>(dst + part * C::P_PART_BYTES) =
+                                    make_uint2(upper_bytes(h[0], h[1]), upper_bytes(h[2], h[3]));
+                            else
+                                *reinterpret_cast<uint32_t*>(dst + part * C::P_PART_BYTES) = upper_bytes(h[0], h[1]);
                         }
-                        float top = -INFINITY;
+                    };
+
+                    const bool ok = mbar_wait(&misc.s_full[slot], parity);
+                    tc_fence_after();
+                    read_scores();
+                    bool raise = j == tb;  // the first tile sets the references
+                    if (!raise) {
+                        less_references();
+                        float top = z[0];
 #pragma unroll
-                        for (int i = 0; i < HG; ++i) {
-                            z[i] -= m[i];
-                            top = fmaxf(top, z[i]);
-                        }
+                        for (int i = 1; i < HG; ++i) top = fmaxf(top, z[i]);
                         const bool need = __any_sync(0xffffffffu, top > kBase + kRescaleLog2 || !ok);
                         if (lane == 0) {
-                            if (need) *reinterpret_cast<volatile int*>(&misc.raise[sg][slot]) = 1;
-                            mbar_arrive(&misc.vote[sg][slot]);
+                            if (need) *reinterpret_cast<volatile int*>(&misc.raise[sg][tcnt & 1]) = 1;
+                            mbar_arrive(&misc.vote[sg]);
                         }
-                        write_weights(slot, z);
-                        // (every warp votes: what it waits for before is bounded well below this)
-                        const bool ok1 = mbar_wait(&misc.vote[sg][slot], parity, 8000000000ull);
-                        if (!ok1 || *reinterpret_cast<volatile int*>(&misc.raise[sg][slot]) != 0) {
-                            // all four warps: exact column maxima, new references, O and l at
-                            // them, the weights again
-                            if (!ok1 || named_bar_or_id<128>(gbar, !ok)) {
+                        write_weights();
+                    } else if (lane == 0) {
+                        mbar_arrive(&misc.vote[sg]);
+                    }
+                    // (every warp votes: what it waits for before is bounded well below this)
+                    const bool ok1 = mbar_wait(&misc.vote[sg], tcnt & 1, 8000000000ull);
+                    raise |= *reinterpret_cast<volatile int*>(&misc.raise[sg][tcnt & 1]) != 0;
+                    if (!ok1 || raise) {
+                        // all four warps: exact column maxima, new references, O and l at
+                        // them, the weights again
+                        if (!ok1 || named_bar_or_id<128>(gbar, !ok)) {
+                            dead = true;
+                            break;
+                        }
+                        if (j > tb) read_scores();
+                        constexpr int SPAN = 32 / HG;
+                        const float v = warp_colmax<HG>(z, lane);
+                        if ((lane & (SPAN - 1)) == 0) misc.red_max[sg][quad][lane / SPAN] = v;
+                        if (row == 0) misc.raise[sg][tcnt & 1] = 0;  // (all have read it before the barrier above)
+                        named_bar_sync_id<128>(gbar);
+                        if (row < HG) {
+                            const float t = fmaxf(fmaxf(misc.red_max[sg][0][row], misc.red_max[sg][1][row]),
+                                                  fmaxf(misc.red_max[sg][2][row], misc.red_max[sg][3][row])) - kBase;
+                            const float m = misc.m_run[sg][row], mnew = j == tb ? t : fmaxf(m, t);
+                            misc.alpha[sg][row] = j == tb ? 1.f : fast_exp2(m - mnew);
+                            misc.m_run[sg][row] = mnew;  // (all have read the old one before the barrier above)
+                        }
+                        named_bar_sync_id<128>(gbar);
+                        if (j > tb) {
+                            // O holds earlier tiles of the range: rescaled once their output MMAs are
+                            // done (the last one of this branch is a tile back)
+                            const uint32_t before = gs - C::NSTEP;
+                            const bool ok2 = mbar_wait(&misc.p_empty[before % C::NSP], (before / C::NSP) & 1);
+                            if (named_bar_or_id<128>(gbar, !ok2)) {
                                 dead = true;
                                 break;
                             }
-                            read_scores(slot, k, ls, masked, z);
-                            constexpr int SPAN = 32 / HG;
-                            const float v = warp_colmax<HG>(z, lane);
-                            if ((lane & (SPAN - 1)) == 0) misc.red_max[sg][quad][lane / SPAN] = v;
-                            named_bar_sync_id<128>(gbar);
-                            float alpha[HG];
+                            tc_fence_after();
 #pragma unroll
-                            for (int i = 0; i < HG; ++i) {
-                                const float t = fmaxf(fmaxf(misc.red_max[sg][0][i], misc.red_max[sg][1][i]),
-                                                      fmaxf(misc.red_max[sg][2][i], misc.red_max[sg][3][i]));
-                                const float mnew = fmaxf(m[i], t - kBase);
-                                alpha[i] = fast_exp2(m[i] - mnew);
-                                m[i] = mnew;
-                                l[0][i] *= alpha[i];
-                                z[i] -= mnew;
-                            }
-                            // (everyone has read the old references before the barrier above)
-                            if (stid == 0) {
-#pragma unroll
-                                for (int i = 0; i < HG; ++i) m_step[i] = m[i];
-                                misc.raise[sg][slot] = 0;
-                            }
-                            named_bar_sync_id<128>(gbar);
-                            if (j > tb) {
-                                const bool ok2 = mbar_wait(&misc.p_empty[(gs - 1) % C::NSP], ((gs - 1) / C::NSP) & 1);
-                                if (named_bar_or_id<128>(gbar, !ok2)) {
-                                    dead = true;
-                                    break;
-                                }
-                                tc_fence_after();
+                            for (int i = 0; i < HG; ++i) l[i] *= misc.alpha[sg][i];
 #pragma unroll 1
-                                for (int e = 0; e < C::CPS * C::BPC * 3; ++e) {
-                                    const int part = e % 3, c = e / 3 / C::BPC, g2 = e / 3 % C::BPC;
-                                    if (C::BY_BRANCH && (DC == 64 ? g2 : c * 128 / DC) != sg) continue;
-                                    const uint32_t at = tmem + lane_off + ((st * C::CPS + c) * C::BPC + g2) * kPN + part * kHP + hoff;
+                            for (int e = 0; e < C::CPS * C::BPC; ++e) {
+                                const int c = e / C::BPC, g2 = e % C::BPC;
+                                if ((DC == 64 ? g2 : c * 128 / DC) != bsel) continue;
+#pragma unroll
+                                for (int part = 0; part < 3; ++part) {
+                                    const uint32_t at = lanes + ((st * C::CPS + c) * C::BPC + g2) * kPN + part * kHP + hoff;
                                     float o[HG];
                                     tmem_ld_cols<HG>(at, o);
                                     tmem_wait_ld();
 #pragma unroll
-                                    for (int i = 0; i < HG; ++i) o[i] *= alpha[i];
+                                    for (int i = 0; i < HG; ++i) o[i] *= misc.alpha[sg][i];
                                     tmem_st_cols<HG>(at, o);
                                 }
-                                tmem_wait_st();
                             }
-                            write_weights(slot, z);
+                            tmem_wait_st();
                         }
-#pragma unroll
-                        for (int i = 0; i < HG; ++i) l[0][i] = fmaf(z[i], rs, l[0][i]);
-                        // rows past the end of the sequence become zero before the output MMA
-                        // reads them: this group clears its half of each row
-                        if (masked) {
-#pragma unroll
-                            for (int c = 0; c < C::CPS; ++c) {
-                                uint8_t* p = sm + C::OFF_CHUNK + ((gs * C::CPS + c) % C::NSTAGE) * C::CHUNK_BYTES + row * 128 + sg * 64;
-#pragma unroll
-                                for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(p + u * 16) = make_uint4(0u, 0u, 0u, 0u);
-                            }
-                        }
-                        fence_proxy_async_smem();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&misc.p_full[slot]);
-                        // the next step's branch first (the step loop is not unrolled: its code
-                        // has to stay in the instruction cache)
-                        if constexpr (C::NSTEP == 2) {
-#pragma unroll
-                            for (int i = 0; i < HG; ++i) {
-                                const float t = l[0][i];
-                                l[0][i] = l[1][i];
-                                l[1][i] = t;
-                            }
-                            const float t = sig[0];
-                            sig[0] = sig[1];
-                            sig[1] = t;
-                        }
-                        ++gs;
+                        read_scores();
+                        less_references();
+                        write_weights();
                     }
 #pragma unroll
-                    for (int st = 0; st < C::NSTEP; ++st) sig[st] = sig_next[st];
-                    ++tcnt;
+                    for (int i = 0; i < HG; ++i) l[i] = fmaf(z[i], rs, l[i]);
+                    // rows past the end of the sequence become zero before the output MMA
+                    // reads them: each group of the step clears its share of each row
+                    if (masked) {
+                        constexpr int BYTES = 128 / C::GPS;
+#pragma unroll
+                        for (int c = 0; c < C::CPS; ++c) {
+                            uint8_t* p = sm + C::OFF_CHUNK + ((gs * C::CPS + c) % C::NSTAGE) * C::CHUNK_BYTES + row * 128 + sg % C::GPS * BYTES;
+#pragma unroll
+                            for (int u = 0; u < BYTES / 16; ++u) *reinterpret_cast<uint4*>(p + u * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&misc.p_full[slot]);
+                    sig = sig_next;
                 }
                 if (dead) continue;
 
                 // ---------------------------------------------------- epilogue
-                constexpr int NV = C::NSTEP * HG;  // (branch, head) values of the group
                 {
-                    float f[NV];
+                    float f[HG];
 #pragma unroll
-                    for (int st = 0; st < C::NSTEP; ++st)
-#pragma unroll
-                        for (int i = 0; i < HG; ++i) f[st * HG + i] = l[st][i];
-                    warp_sum_scatter<NV, 16, NV>(f, lane);
-                    constexpr int SPAN = 32 / NV;
-                    if ((lane & (SPAN - 1)) == 0) misc.red_sum[quad][NV * sg + lane / SPAN] = f[0];
+                    for (int i = 0; i < HG; ++i) f[i] = l[i];
+                    warp_sum_scatter<HG, 16, HG>(f, lane);
+                    constexpr int SPAN = 32 / HG;
+                    if ((lane & (SPAN - 1)) == 0) misc.red_sum[sg][quad][lane / SPAN] = f[0];
                 }
                 bad = named_bar_or_id<128>(gbar, bad);  // also publishes red_sum
                 const bool single = cum >= A0 && cum + (tiles - 1) * kTileCost < A1;
                 const size_t slot = (size_t)grp.slot0 + grp.ci + n;
-                if (stid < NV) {
-                    const int c = NV * sg + stid;
-                    const float lt = misc.red_sum[0][c] + misc.red_sum[1][c] + misc.red_sum[2][c] + misc.red_sum[3][c];
-                    const int b = stid / HG * C::SBR + bsel, i = hoff + stid % HG;
-                    misc.inv_l[b * kHP + i] = 1.0f / lt;
+                if (row < HG) {
+                    const float lt = misc.red_sum[sg][0][row] + misc.red_sum[sg][1][row] + misc.red_sum[sg][2][row] + misc.red_sum[sg][3][row];
+                    misc.inv_l[sg][row] = 1.0f / lt;
                     if (!single)
-                        a.lse_part[(slot * NB + b) * kHP + i] = bad ? bad_split_marker() : misc.m_run[b * kHP + i] + __log2f(lt);
+                        a.lse_part[(slot * NB + br) * kHP + hoff + row] = bad ? bad_split_marker() : misc.m_run[sg][row] + __log2f(lt);
                 }
                 {
-                    const bool ok = mbar_wait(&misc.p_empty[(gs - 1) % C::NSP], ((gs - 1) / C::NSP) & 1);
+                    const uint32_t last = (tcnt - 1) * C::NSTEP + st;
+                    const bool ok = mbar_wait(&misc.p_empty[last % C::NSP], (last / C::NSP) & 1);
                     if (named_bar_or_id<128>(gbar, !ok)) {
                         dead = true;
                         continue;
@@ -785,56 +763,60 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                 }
                 tc_fence_after();
                 constexpr int WIDTH = DC >= 128 ? 128 : DC;  // valid rows of an output block
+#pragma unroll 1
+                for (int e = 0; e < C::CPS * C::BPC; ++e) {
+                    const int c = e / C::BPC, g2 = e % C::BPC;
+                    if ((DC == 64 ? g2 : c * 128 / DC) != bsel) continue;
+                    const uint32_t at = lanes + ((st * C::CPS + c) * C::BPC + g2) * kPN + hoff;
+                    const int first = g2 * WIDTH;  // valid rows: this branch's of a shared chunk
+                    const bool mine = row >= first && row < first + WIDTH;
+                    const int col = DC >= 128 ? c * 128 % DC + row : row - first;  // latent column
+                    constexpr int N = HG < 8 ? HG : 8;
 #pragma unroll
-                for (int blk = 0; blk < C::O_BLOCKS; ++blk) {
-                    const int g2 = blk % C::BPC, gp = blk / C::BPC;
-                    const int first = g2 * WIDTH;
-                    const int b = (gp * 128 + first) / DC;
-                    const int k = (gp * 128 + first) % DC + (row - first);
-                    if (C::BY_BRANCH && b % C::SBR != sg) continue;
-                    float o[HG], o1[HG], o2[HG];
-                    tmem_ld_cols<HG>(tmem + lane_off + blk * kPN + hoff, o);
-                    tmem_ld_cols<HG>(tmem + lane_off + blk * kPN + kHP + hoff, o1);
-                    tmem_ld_cols<HG>(tmem + lane_off + blk * kPN + 2 * kHP + hoff, o2);
-                    tmem_wait_ld();
-                    if (row < first || row >= first + WIDTH) continue;
-                    const float* inv = &misc.inv_l[b * kHP + hoff];
+                    for (int i0 = 0; i0 < HG; i0 += N) {
+                        float o[N], o1[N], o2[N];
+                        tmem_ld_cols<N>(at + i0, o);
+                        tmem_ld_cols<N>(at + kHP + i0, o1);
+                        tmem_ld_cols<N>(at + 2 * kHP + i0, o2);
+                        tmem_wait_ld();
+                        if (!mine) continue;
 #pragma unroll
-                    for (int i = 0; i < HG; ++i) o[i] = bad ? 0.f : (o[i] + (o1[i] + o2[i])) * inv[i];
-                    if (single) {
-                        __nv_bfloat16* dst = a.out + (((size_t)n * H + grp.h0 + hoff) * NB + b) * DC + k;
+                        for (int i = 0; i < N; ++i) o[i] = bad ? 0.f : (o[i] + (o1[i] + o2[i])) * misc.inv_l[sg][i0 + i];
+                        if (single) {
+                            const int h0 = hoff + i0;
+                            __nv_bfloat16* dst = a.out + (((size_t)n * H + grp.h0 + h0) * NB + br) * DC + col;
 #pragma unroll
-                        for (int i = 0; i < HG; ++i)
-                            if (hoff + i < grp.hn) dst[(size_t)i * C::W] = to_bf16(o[i] * a.out_scale);
-                    } else {
-                        float* dst = a.o_part + ((slot * NB + b) * DC + k) * kHP + hoff;
-#pragma unroll
-                        for (int i = 0; i < HG; i += 8)
-                            st_global_v8(dst + i, o[i], o[i + 1], o[i + 2], o[i + 3], o[i + 4], o[i + 5], o[i + 6], o[i + 7]);
+                            for (int i = 0; i < N; ++i)
+                                if (h0 + i < grp.hn) dst[(size_t)i * C::W] = to_bf16(o[i] * a.out_scale);
+                        } else {
+                            float* dst = a.o_part + ((slot * NB + br) * DC + col) * kHP + hoff + i0;
+                            if constexpr (N == 4)
+                                *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
+                            else
+                                st_global_v8(dst, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
+                        }
                     }
                 }
-                if (bad && stid == 0) record_error(a.err, MLRA_ERR_DEVICE_BAD_INDEX);
+                if (bad && row == 0) record_error(a.err, MLRA_ERR_DEVICE_BAD_INDEX);
                 tc_fence_before();
                 named_bar_sync_id<128>(gbar);  // inv_l and red_sum are reused by the next range
-                if (stid == 0) {
+                if (threadIdx.x == 128) {
                     if (!single) {
                         if (pend_a < 0) pend_a = n; else pend_b = n;
                     }
-                    if (sg == 0) {
-                        misc.last_seg[0] = n;
-                        misc.last_seg[1] = cum;
-                        misc.last_seg[2] = tiles;
-                        misc.last_seg[3] = c1_member;
-                    }
+                    misc.last_seg[0] = n;
+                    misc.last_seg[1] = cum;
+                    misc.last_seg[2] = tiles;
+                    misc.last_seg[3] = c1_member;
                 }
             }
-            if (dead && stid == 0) {
+            if (dead && row == 0) {
                 record_error(a.err, MLRA_ERR_DEVICE_TIMEOUT);
                 *abort_flag = 1;
             }
-            // both groups' partial stores, then one release fence, then the counts
-            const bool any_dead = named_bar_or<6, 256>(dead);
-            if (!any_dead && sg == 0 && stid == 0 && pend_a >= 0) {
+            // every group's partial stores, then one release fence, then the counts
+            const bool any_dead = named_bar_or<6, kSoft>(dead);
+            if (!any_dead && threadIdx.x == 128 && pend_a >= 0) {
                 fence_acq_rel_gpu();
                 red_add_relaxed_gpu(a.seq_cnt + grp.cnt0 + pend_a, 1);
                 if (pend_b >= 0) red_add_relaxed_gpu(a.seq_cnt + grp.cnt0 + pend_b, 1);
@@ -847,7 +829,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
     if (*abort_flag) return;
-    merge_tail<NB, DC, kHP>(a, grp, misc.last_seg[0], misc.last_seg[1], misc.last_seg[2], misc.last_seg[3] != 0, chunk,
+    merge_tail<NB, DC, kHP, kFp8Threads>(a, grp, misc.last_seg[0], misc.last_seg[1], misc.last_seg[2], misc.last_seg[3] != 0, chunk,
                             reinterpret_cast<float*>(sm + C::OFF_CHUNK), &misc.merge_flag, &misc.merge_full);
 }
 
@@ -870,7 +852,7 @@ cudaError_t launch_cfg(const DecodeArgs& a, const float* latent_scale, cudaStrea
     // cooperative: every CTA is resident, so the merge's waits end
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.num_ctas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kFp8Threads);
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];

@@ -108,23 +108,43 @@ __device__ __forceinline__ float warp_colmax8(const float (&v)[8], int lane) {
     return fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 1));
 }
 
-// The same for a softmax group's N = 8 or 16 heads: column c in lanes
+// And of 4 values: column c in lanes 8c..8c+7.  6 shuffles.
+__device__ __forceinline__ float warp_colmax4(const float (&v)[4], int lane) {
+    float a2[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // lanes with bit 4 keep columns 2..3
+        const bool hi = lane & 16;
+        const float keep = hi ? v[i + 2] : v[i], send = hi ? v[i] : v[i + 2];
+        a2[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, 16));
+    }
+    const bool hi = lane & 8;
+    const float keep = hi ? a2[1] : a2[0], send = hi ? a2[0] : a2[1];
+    float a1 = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, 8));
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, o));
+    return a1;
+}
+
+// The same for a softmax group's N = 4, 8 or 16 heads: column c in lanes
 // [c 32 / N, (c + 1) 32 / N).
 template <int N>
 __device__ __forceinline__ float warp_colmax(const float (&v)[N], int lane) {
-    if constexpr (N == 8) return warp_colmax8(v, lane);
+    if constexpr (N == 4) return warp_colmax4(v, lane);
+    else if constexpr (N == 8) return warp_colmax8(v, lane);
     else return warp_colmax16(v, lane);
 }
 
-// TMEM loads and stores of a softmax group's N = 8 or 16 columns.
+// TMEM loads and stores of a softmax group's N = 4, 8 or 16 columns.
 template <int N>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[N]) {
-    if constexpr (N == 8) tmem_ld8(taddr, v);
+    if constexpr (N == 4) tmem_ld4(taddr, v);
+    else if constexpr (N == 8) tmem_ld8(taddr, v);
     else tmem_ld16(taddr, v);
 }
 template <int N>
 __device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const float (&v)[N]) {
-    if constexpr (N == 8) tmem_st8(taddr, v);
+    if constexpr (N == 4) tmem_st4(taddr, v);
+    else if constexpr (N == 8) tmem_st8(taddr, v);
     else tmem_st16(taddr, v);
 }
 
@@ -216,7 +236,7 @@ __device__ __forceinline__ int next_range_seq(const DecodeArgs& a, int n, int cu
 // and the last of the S + G counts returns seq_cnt[n] to zero.  The arithmetic
 // is laid out for latency: every thread loads its values for up to 8 splits
 // at once before combining them.
-template <int NB, int DC, int HP>
+template <int NB, int DC, int HP, int THREADS = kThreads>
 __device__ __forceinline__ void merge_tail(const DecodeArgs& a, const HeadGroup& grp, int n, int cum, int tiles,
                                            bool c1_member, int chunk, float* w_s, int* flag, uint64_t* bar) {
     constexpr int kHP = HP;
@@ -285,7 +305,7 @@ __device__ __forceinline__ void merge_tail(const DecodeArgs& a, const HeadGroup&
     }
     // weights out_scale * 2^(lse - max) / sum, two threads per (branch, head)
     // column, each over every other split, eight splits' values in flight
-    static_assert(2 * HB <= kThreads && HB % 16 == 0, "two threads per column in whole warps");
+    static_assert(2 * HB <= THREADS && HB % 16 == 0, "two threads per column in whole warps");
     if (tid < 2 * HB) {
         const int col = tid >> 1, half = tid & 1;
         float mx = -INFINITY;
@@ -331,7 +351,7 @@ __device__ __forceinline__ void merge_tail(const DecodeArgs& a, const HeadGroup&
 
     // items (row, head quad), quads fastest: conflict-free 16-byte reads; the
     // weighted sum over the splits in split order, eight splits' loads at once
-    for (int e = tid; e < rows * QD; e += kThreads) {
+    for (int e = tid; e < rows * QD; e += THREADS) {
         const int lr = e / QD, q = e % QD, row = r0 + lr;
         const int b = row / DC, k = row % DC;
         const float* w = w_s + b * kHP + 4 * q;

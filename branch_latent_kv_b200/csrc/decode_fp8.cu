@@ -31,7 +31,9 @@
 //
 // Softmax: four groups of four warps, each the owner of one branch's 16 heads
 // (of half of them with two branches, a quarter with one), a thread having
-// one token of the tile.  With half the bytes a tile lasts 1.9 us at HBM's
+// one token of the tile.  A branch of a tile is one step of the pipeline
+// (score MMA, softmax, output MMA), so a chunk of latents leaves its place in
+// the ring as soon as its own branch is done.  With half the bytes a tile lasts 1.9 us at HBM's
 // rate, less than one group takes for two branches (2.1 us, the two-group
 // layout of decode_tc.cu), so the branches are worked on side by side.
 // The four warps of a group share the reference M of each head, which a warp
@@ -55,7 +57,8 @@ namespace {
 constexpr int kHP = 16;       // heads per tile
 constexpr int kSN = 2 * kHP;  // score columns of a branch: hi and lo query parts
 constexpr int kPN = 3 * kHP;  // output columns of a block: three probability parts
-constexpr int kMaxStages = 16;
+constexpr int kMaxStages = 10;
+constexpr int kMaxSteps = 5;
 // the reference M sits 2^kBase below the largest weight when it is set, and a
 // weight may pass that by 2^kRescaleLog2: at most 2^15, e5m2 holds 1.75 2^15
 constexpr float kBase = 7.0f;
@@ -68,7 +71,7 @@ struct Cfg {
     static constexpr int W = NB * DC;                            // latent bytes per token
     static constexpr int NCH = W / 128;                          // 128-byte chunks of a token row
     static constexpr int BPC = DC >= 128 ? 1 : 128 / DC;         // branches per chunk
-    static constexpr int SBR = NB == 1 ? 1 : 2;                  // branches per step
+    static constexpr int SBR = BPC;                              // branches per step (a chunk is not divided)
     static constexpr int HG = kHP * NB / kGroups;                // heads of a softmax group: 16, 8 or 4
     static constexpr int GPB = kGroups / NB;                     // groups per branch
     static constexpr int GPS = GPB * SBR;                        // groups per step
@@ -83,12 +86,13 @@ struct Cfg {
     static constexpr int P_PART_BYTES = kT * kHP;                // one part of one branch
     static constexpr int P_BRANCH_BYTES = 3 * P_PART_BYTES;
     static constexpr int P_BYTES = SBR * P_BRANCH_BYTES;
-    static constexpr int MISC_BYTES = 4096;
-    // steps between their score MMA and their output MMA; RoPE tiles in
-    // flight (three where a tile is one chunk or two); RoPE score slots
-    static constexpr int NSP = NSTEP == 1 && CPS == 1 ? 4 : 3;
+    static constexpr int MISC_BYTES = 2048;
+    // steps between their score MMA and their output MMA (a tile's and one
+    // more); RoPE tiles in flight (more where a tile is a chunk or two); RoPE
+    // score slots (one is written again when the steps that read it are over)
+    static constexpr int NSP = NSTEP == 4 ? 5 : SBR == 2 ? 3 : 4;
     static constexpr int NROPE = NCH >= 4 ? 2 : NCH == 2 ? 3 : 4;
-    static constexpr int NRS = (NSP + NSTEP - 1) / NSTEP > 2 ? (NSP + NSTEP - 1) / NSTEP : 2;
+    static constexpr int NRS = (NSP + 2 * NSTEP - 2) / NSTEP > 2 ? (NSP + 2 * NSTEP - 2) / NSTEP : 2;
     static constexpr int FIXED = NROPE * ROPE_BYTES + Q_BYTES + QR_SPAN + NSP * P_BYTES + MISC_BYTES;
     static constexpr int NSTAGE_FIT = (kSmemLimit - 1024 - FIXED) / CHUNK_BYTES;
     static constexpr int NSTAGE = NSTAGE_FIT > kMaxStages ? kMaxStages : NSTAGE_FIT;
@@ -108,7 +112,7 @@ struct Cfg {
     static constexpr int TMEM_COLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
     static_assert(NRS * NSTEP >= NSP + NSTEP - 1, "a RoPE score is read before its slot is written again");
     static_assert(NB % SBR == 0 && SBR * DC % 128 == 0 && NSTEP * CPS == NCH, "steps fill whole chunks");
-    static_assert(CPS >= 1 && NSTAGE >= 2 * CPS && NROPE <= 4 && NSP <= 4, "rings");
+    static_assert(CPS >= 1 && NSTAGE >= 2 * CPS && NROPE <= 4 && NSP <= kMaxSteps, "rings");
     static_assert(COLS <= 512 && SMEM_BYTES <= kSmemLimit, "TMEM and shared memory");
     static_assert(Q_BYTES % 1024 == 0 && ROPE_BYTES % 1024 == 0 && P_BYTES % 1024 == 0, "regions stay aligned");
 };
@@ -118,9 +122,9 @@ struct Misc {
     uint64_t chunk_empty[kMaxStages];
     uint64_t rope_full[4];
     uint64_t rope_empty[4];
-    uint64_t s_full[4];   // step g in slot g % NSP: its scores are in TMEM
-    uint64_t p_full[4];   // its probabilities are in shared memory
-    uint64_t p_empty[4];  // its output MMA finished
+    uint64_t s_full[kMaxSteps];   // step g in slot g % NSP: its scores are in TMEM
+    uint64_t p_full[kMaxSteps];   // its probabilities are in shared memory
+    uint64_t p_empty[kMaxSteps];  // its output MMA finished
     uint64_t vote[kGroups];  // a group's four warps have voted on a tile
     uint64_t q_full;      // a range's queries are in shared memory (written by the softmax warps)
     uint64_t drain[2];
@@ -131,14 +135,11 @@ struct Misc {
     int last_seg[4];
     int merge_flag;
     int raise[kGroups][2];    // tile t (t & 1): some warp of the group needs a higher reference
-    float q_max[4 * kGroups]; // largest query magnitude seen by each softmax warp
-    float red_max[kGroups][4][kHP];  // [group][quadrant][head]
-    float red_sum[kGroups][4][kHP];
-    float inv_l[kGroups][kHP];
+    float red[kGroups][4][kHP];       // [group][quadrant][head]: maxima of a raise, at the end sums
     alignas(16) float m_run[kGroups][kHP];  // references M; read as float4
-    alignas(16) float alpha[kGroups][kHP];  // a raise: what O and l shrink by
+    float factor[kGroups][kHP];       // a range's start: largest query magnitude of each warp; a raise: what O and l shrink by; its end: 1 / l
 };
-static_assert(offsetof(Misc, m_run) % 16 == 0 && offsetof(Misc, alpha) % 16 == 0, "float4 access");
+static_assert(offsetof(Misc, m_run) % 16 == 0, "float4 access");
 
 struct Maps {
     CUtensorMap lat;   // latent bytes [pages * P][W]
@@ -501,14 +502,15 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                         }
                     }
                     mx = __reduce_max_sync(0xffffffffu, mx);
-                    if (lane == 0) misc.q_max[warp - 4] = __uint_as_float(mx << 16);
+                    if (lane == 0) misc.factor[sg][quad] = __uint_as_float(mx << 16);
                     if (named_bar_or<5, kSoft>(dead)) {
                         dead = true;
                         break;
                     }
-                    float top = misc.q_max[0];
+                    // (factor is written again at the first tile, whose scores wait for q_full)
+                    float top = 0.f;
 #pragma unroll
-                    for (int i = 1; i < 4 * kGroups; ++i) top = fmaxf(top, misc.q_max[i]);
+                    for (int i = 0; i < 4 * kGroups; ++i) top = fmaxf(top, misc.factor[i / 4][i % 4]);
                     // the smallest power of two tau with top <= 448 tau (2^-100 at least: both it
                     // and its reciprocal are normal numbers)
                     const uint32_t tb32 = __float_as_uint(top);
@@ -670,14 +672,14 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                         if (j > tb) read_scores();
                         constexpr int SPAN = 32 / HG;
                         const float v = warp_colmax<HG>(z, lane);
-                        if ((lane & (SPAN - 1)) == 0) misc.red_max[sg][quad][lane / SPAN] = v;
+                        if ((lane & (SPAN - 1)) == 0) misc.red[sg][quad][lane / SPAN] = v;
                         if (row == 0) misc.raise[sg][tcnt & 1] = 0;  // (all have read it before the barrier above)
                         named_bar_sync_id<128>(gbar);
                         if (row < HG) {
-                            const float t = fmaxf(fmaxf(misc.red_max[sg][0][row], misc.red_max[sg][1][row]),
-                                                  fmaxf(misc.red_max[sg][2][row], misc.red_max[sg][3][row])) - kBase;
+                            const float t = fmaxf(fmaxf(misc.red[sg][0][row], misc.red[sg][1][row]),
+                                                  fmaxf(misc.red[sg][2][row], misc.red[sg][3][row])) - kBase;
                             const float m = misc.m_run[sg][row], mnew = j == tb ? t : fmaxf(m, t);
-                            misc.alpha[sg][row] = j == tb ? 1.f : fast_exp2(m - mnew);
+                            misc.factor[sg][row] = j == tb ? 1.f : fast_exp2(m - mnew);
                             misc.m_run[sg][row] = mnew;  // (all have read the old one before the barrier above)
                         }
                         named_bar_sync_id<128>(gbar);
@@ -692,7 +694,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                             }
                             tc_fence_after();
 #pragma unroll
-                            for (int i = 0; i < HG; ++i) l[i] *= misc.alpha[sg][i];
+                            for (int i = 0; i < HG; ++i) l[i] *= misc.factor[sg][i];
 #pragma unroll 1
                             for (int e = 0; e < C::CPS * C::BPC; ++e) {
                                 const int c = e / C::BPC, g2 = e % C::BPC;
@@ -704,7 +706,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                                     tmem_ld_cols<HG>(at, o);
                                     tmem_wait_ld();
 #pragma unroll
-                                    for (int i = 0; i < HG; ++i) o[i] *= misc.alpha[sg][i];
+                                    for (int i = 0; i < HG; ++i) o[i] *= misc.factor[sg][i];
                                     tmem_st_cols<HG>(at, o);
                                 }
                             }
@@ -742,14 +744,14 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                     for (int i = 0; i < HG; ++i) f[i] = l[i];
                     warp_sum_scatter<HG, 16, HG>(f, lane);
                     constexpr int SPAN = 32 / HG;
-                    if ((lane & (SPAN - 1)) == 0) misc.red_sum[sg][quad][lane / SPAN] = f[0];
+                    if ((lane & (SPAN - 1)) == 0) misc.red[sg][quad][lane / SPAN] = f[0];
                 }
-                bad = named_bar_or_id<128>(gbar, bad);  // also publishes red_sum
+                bad = named_bar_or_id<128>(gbar, bad);  // also publishes red
                 const bool single = cum >= A0 && cum + (tiles - 1) * kTileCost < A1;
                 const size_t slot = (size_t)grp.slot0 + grp.ci + n;
                 if (row < HG) {
-                    const float lt = misc.red_sum[sg][0][row] + misc.red_sum[sg][1][row] + misc.red_sum[sg][2][row] + misc.red_sum[sg][3][row];
-                    misc.inv_l[sg][row] = 1.0f / lt;
+                    const float lt = misc.red[sg][0][row] + misc.red[sg][1][row] + misc.red[sg][2][row] + misc.red[sg][3][row];
+                    misc.factor[sg][row] = 1.0f / lt;
                     if (!single)
                         a.lse_part[(slot * NB + br) * kHP + hoff + row] = bad ? bad_split_marker() : misc.m_run[sg][row] + __log2f(lt);
                 }
@@ -781,7 +783,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                         tmem_wait_ld();
                         if (!mine) continue;
 #pragma unroll
-                        for (int i = 0; i < N; ++i) o[i] = bad ? 0.f : (o[i] + (o1[i] + o2[i])) * misc.inv_l[sg][i0 + i];
+                        for (int i = 0; i < N; ++i) o[i] = bad ? 0.f : (o[i] + (o1[i] + o2[i])) * misc.factor[sg][i0 + i];
                         if (single) {
                             const int h0 = hoff + i0;
                             __nv_bfloat16* dst = a.out + (((size_t)n * H + grp.h0 + h0) * NB + br) * DC + col;
@@ -799,7 +801,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                 }
                 if (bad && row == 0) record_error(a.err, MLRA_ERR_DEVICE_BAD_INDEX);
                 tc_fence_before();
-                named_bar_sync_id<128>(gbar);  // inv_l and red_sum are reused by the next range
+                named_bar_sync_id<128>(gbar);  // factor and red are reused by the next range
                 if (threadIdx.x == 128) {
                     if (!single) {
                         if (pend_a < 0) pend_a = n; else pend_b = n;

@@ -10,7 +10,6 @@ first call raises immediately.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import threading
 from typing import Optional
@@ -406,74 +405,46 @@ def mlra_prepare(q_c, q_r, w_uk, c_new, kr_new, seqlens, block_table, latent_cac
 MLRA_FP8_BLOCK = 16  # tokens of a page that share one scale per branch
 
 
-def _arg(t, name: str, dtype: torch.dtype, shape, device: torch.device) -> int:
-    """The data pointer of a contiguous tensor of this type, shape and device."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+_launch_module = None
 
 
-def _cuda_device(t, name: str, ndim: int, where: str) -> torch.device:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != ndim:
-        raise ValueError(f"{name} must have {ndim} dimensions, got shape {tuple(t.shape)}")
-    if t.device.type != "cuda":
-        raise ValueError(f"{where} runs on CUDA tensors only")
-    return t.device
-
-
-def _launch(entry: str, device: torch.device, *args) -> None:
-    """Calls a launching entry with `device` current (the library launches on
-    the current device) and raises on a non-OK status."""
-    fn = getattr(library(), entry)
-    if device.index == torch.cuda.current_device():
-        st = fn(*args)
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args)
-    _check(st, entry)
-
-
-def _stream_workspace(dims: mlra_dims, device: torch.device, stream) -> torch.Tensor:
-    """The default workspace of a call on `stream` (None: the current one):
-    mlra_decode's own on the legacy default stream, one for each other stream,
-    and one for each call under graph capture, so that neither calls on
-    different streams nor replays of different graphs share one."""
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    capturing = torch.cuda.is_current_stream_capturing()
-    if s.cuda_stream == 0 and not capturing:
-        return workspace_for(dims, device)
-    need = _workspace_bytes(dims)
-    key = (device.index, s.cuda_stream)
-    ws = None if capturing else _ws_cache.get(key)
-    if ws is None or ws.numel() < need:
-        with torch.cuda.stream(s):
-            ws = torch.empty(need, dtype=torch.uint8, device=device)
-            ws[:_WS_HEAD].zero_()
-        if not capturing:
-            _ws_cache[key] = ws
-    return ws
+def _launches():
+    """The checked launches of these entries (``csrc/launch_ext.cpp``), bound
+    to the loaded library; raises if the module has not been built."""
+    global _launch_module
+    if _launch_module is None:
+        lib = library()
+        try:
+            from . import _launch as module
+        except ImportError as e:
+            raise RuntimeError(f"{_PKG}/_launch.so is missing or does not load; build it with "
+                               "`python -m branch_latent_kv_b200.build`") from e
+        module.bind(MlraError, _ws_cache, _new_workspace,
+                    *(ctypes.cast(f, ctypes.c_void_p).value for f in
+                      (lib.mlra_prefill, lib.mlra_append_fp8, lib.mlra_decode_fp8, lib.mlra_decode_workspace_bytes)))
+        _launch_module = module
+    return _launch_module
 
 
 _WS_HEAD = 256 + 4 * 65536  # the error word and the split counters, the part that must start at zero
 
 
-@functools.lru_cache(maxsize=256)
-def _workspace_bytes_of(*dims: int) -> int:
-    return mlra_decode_workspace_bytes(mlra_dims(*dims))
-
-
-def _workspace_bytes(d: mlra_dims) -> int:
-    return _workspace_bytes_of(d.batch, d.heads, d.branches, d.d_c, d.d_r, d.page_size, d.max_pages_per_seq, d.num_pages)
+def _new_workspace(need: int, index: int, stream) -> torch.Tensor:
+    """A first, or larger, default workspace of a call on `stream` (None: the
+    current one): mlra_decode's own on the legacy default stream, one for each
+    other stream, and one for each call under graph capture, so that neither
+    calls on different streams nor replays of different graphs share one."""
+    s = stream if stream is not None else torch.cuda.current_stream(index)
+    with torch.cuda.stream(s):
+        capturing = torch.cuda.is_current_stream_capturing()
+        key = index if s.cuda_stream == 0 else (index, s.cuda_stream)
+        ws = None if capturing else _ws_cache.get(key)
+        if ws is None or ws.numel() < need:
+            ws = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
+            ws[:_WS_HEAD].zero_()
+            if not capturing:
+                _ws_cache[key] = ws
+    return ws
 
 
 def mlra_prefill(q_lat, q_rope, latent_cache, rope_cache, block_table, seqlens, cu_seqlens, scale, out_scale,
@@ -489,29 +460,8 @@ def mlra_prefill(q_lat, q_rope, latent_cache, rope_cache, block_table, seqlens, 
     int32 [N+1]; device_status: optional int32 [1] device tensor receiving the
     first device-detected error code.  Returns out bf16 [T,H,B,d_c].
     """
-    dev = _cuda_device(q_lat, "q_lat", 4, "mlra_prefill")
-    _cuda_device(latent_cache, "latent_cache", 4, "mlra_prefill")
-    T, H, B, d_c = q_lat.shape
-    pages, P = latent_cache.shape[:2]
-    _cuda_device(block_table, "block_table", 2, "mlra_prefill")
-    _cuda_device(q_rope, "q_rope", 3, "mlra_prefill")
-    N, max_pages = block_table.shape
-    d_r = q_rope.shape[2]
-    bf16, i32 = torch.bfloat16, torch.int32
-    p_q = _arg(q_lat, "q_lat", bf16, (T, H, B, d_c), dev)
-    p_qr = _arg(q_rope, "q_rope", bf16, (T, H, d_r), dev)
-    p_lat = _arg(latent_cache, "latent_cache", bf16, (pages, P, B, d_c), dev)
-    p_rope = _arg(rope_cache, "rope_cache", bf16, (pages, P, d_r), dev)
-    p_bt = _arg(block_table, "block_table", i32, (N, max_pages), dev)
-    p_len = _arg(seqlens, "seqlens", i32, (N,), dev)
-    p_cu = _arg(cu_seqlens, "cu_seqlens", i32, (N + 1,), dev)
-    out = torch.empty_like(q_lat) if out is None else out
-    p_out = _arg(out, "out", bf16, (T, H, B, d_c), dev)
-    p_st = None if device_status is None else _arg(device_status, "device_status", i32, (1,), dev)
-    dims = mlra_dims(N, H, B, d_c, d_r, P, max_pages, pages)
-    _launch("mlra_prefill", dev, ctypes.byref(dims), T, p_q, p_qr, p_lat, p_rope, p_bt, p_len, p_cu, float(scale),
-            float(out_scale), p_out, p_st, _stream_ptr(stream, dev))
-    return out
+    return _launches().prefill(q_lat, q_rope, latent_cache, rope_cache, block_table, seqlens, cu_seqlens, scale, out_scale,
+                             out, device_status, stream)
 
 
 def mlra_append_fp8(c_new, kr_new, cu_seqlens, seqlens, block_table, latent_cache, latent_scale, rope_cache,
@@ -527,27 +477,8 @@ def mlra_append_fp8(c_new, kr_new, cu_seqlens, seqlens, block_table, latent_cach
     device_status: optional int32 [1] device tensor receiving the first
     device-detected error code.
     """
-    dev = _cuda_device(c_new, "c_new", 3, "mlra_append_fp8")
-    _cuda_device(latent_cache, "latent_cache", 4, "mlra_append_fp8")
-    T, B, d_c = c_new.shape
-    pages, P = latent_cache.shape[:2]
-    _cuda_device(block_table, "block_table", 2, "mlra_append_fp8")
-    _cuda_device(kr_new, "kr_new", 2, "mlra_append_fp8")
-    N, max_pages = block_table.shape
-    d_r = kr_new.shape[1]
-    bf16, i32 = torch.bfloat16, torch.int32
-    p_c = _arg(c_new, "c_new", bf16, (T, B, d_c), dev)
-    p_kr = _arg(kr_new, "kr_new", bf16, (T, d_r), dev)
-    p_cu = _arg(cu_seqlens, "cu_seqlens", i32, (N + 1,), dev)
-    p_len = _arg(seqlens, "seqlens", i32, (N,), dev)
-    p_bt = _arg(block_table, "block_table", i32, (N, max_pages), dev)
-    p_lat = _arg(latent_cache, "latent_cache", torch.float8_e4m3fn, (pages, P, B, d_c), dev)
-    p_sc = _arg(latent_scale, "latent_scale", torch.float32, (pages, P // MLRA_FP8_BLOCK, B), dev)
-    p_rope = _arg(rope_cache, "rope_cache", bf16, (pages, P, d_r), dev)
-    p_st = None if device_status is None else _arg(device_status, "device_status", i32, (1,), dev)
-    dims = mlra_dims(N, 1, B, d_c, d_r, P, max_pages, pages)
-    _launch("mlra_append_fp8", dev, ctypes.byref(dims), T, p_c, p_kr, p_cu, p_len, p_bt, float(rope_base), p_lat, p_sc,
-            p_rope, p_st, _stream_ptr(stream, dev))
+    _launches().append_fp8(c_new, kr_new, cu_seqlens, seqlens, block_table, latent_cache, latent_scale, rope_cache, rope_base,
+                         device_status, stream)
 
 
 def mlra_decode_fp8(q_lat, q_rope, latent_cache, latent_scale, rope_cache, block_table, seqlens, scale, out_scale,
@@ -560,32 +491,8 @@ def mlra_decode_fp8(q_lat, q_rope, latent_cache, latent_scale, rope_cache, block
     out bf16 [N,H,B,d_c].  Without a workspace the call uses one of its
     stream's (under graph capture one of its own).
     """
-    dev = _cuda_device(q_lat, "q_lat", 4, "mlra_decode_fp8")
-    _cuda_device(latent_cache, "latent_cache", 4, "mlra_decode_fp8")
-    N, H, B, d_c = q_lat.shape
-    pages, P = latent_cache.shape[:2]
-    _cuda_device(block_table, "block_table", 2, "mlra_decode_fp8")
-    _cuda_device(q_rope, "q_rope", 3, "mlra_decode_fp8")
-    max_pages, d_r = block_table.shape[1], q_rope.shape[2]
-    bf16, i32 = torch.bfloat16, torch.int32
-    p_q = _arg(q_lat, "q_lat", bf16, (N, H, B, d_c), dev)
-    p_qr = _arg(q_rope, "q_rope", bf16, (N, H, d_r), dev)
-    p_lat = _arg(latent_cache, "latent_cache", torch.float8_e4m3fn, (pages, P, B, d_c), dev)
-    p_sc = _arg(latent_scale, "latent_scale", torch.float32, (pages, P // MLRA_FP8_BLOCK, B), dev)
-    p_rope = _arg(rope_cache, "rope_cache", bf16, (pages, P, d_r), dev)
-    p_bt = _arg(block_table, "block_table", i32, (N, max_pages), dev)
-    p_len = _arg(seqlens, "seqlens", i32, (N,), dev)
-    out = torch.empty_like(q_lat) if out is None else out
-    p_out = _arg(out, "out", bf16, (N, H, B, d_c), dev)
-    dims = mlra_dims(N, H, B, d_c, d_r, P, max_pages, pages)
-    if workspace is None:
-        workspace = _stream_workspace(dims, dev, stream)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    _launch("mlra_decode_fp8", dev, ctypes.byref(dims), p_q, p_qr, p_lat, p_sc, p_rope, p_bt, p_len, float(scale),
-            float(out_scale), p_out, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            _stream_ptr(stream, dev))
-    return out
+    return _launches().decode_fp8(q_lat, q_rope, latent_cache, latent_scale, rope_cache, block_table, seqlens, scale,
+                                out_scale, out, workspace, stream)
 
 
 # ------------------------------------------------------------------ branch sharding

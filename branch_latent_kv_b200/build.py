@@ -1,4 +1,6 @@
-"""Build the sm_100a CUDA library ``libmlra.so`` in-tree with nvcc.
+"""Build the sm_100a CUDA library ``libmlra.so`` in-tree with nvcc, and the
+CPython module ``_launch.so`` (checked launches, ``csrc/launch_ext.cpp``) with
+g++ against torch's headers.
 
 Usage: ``python -m branch_latent_kv_b200.build`` (also called by the repo's
 ``__graft_entry__.build()``).  Every ``csrc/*.cu`` is compiled for
@@ -16,6 +18,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 LIB = os.path.join(PKG, "libmlra.so")
+EXT = os.path.join(PKG, "_launch.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -27,16 +30,34 @@ def sources():
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(EXT):
         return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) \
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
+    deps = sources() + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) \
         + glob.glob(os.path.join(INCLUDE, "*.h"))
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _ext_commands(obj: str, out: str):
+    """Compile and link commands of the launch module."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               "/usr/local/cuda/include", sysconfig.get_paths()["include"]]
+    flags = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE,
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for p in include:
+        flags += ["-isystem", p]
+    libs = ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    return (["g++", *flags, "-c", os.path.join(CSRC, "launch_ext.cpp"), "-o", obj],
+            ["g++", "-shared", obj, "-o", out, "-L", os.path.join(root, "lib"), *libs])
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile every kernel source and link libmlra.so; returns its path."""
+    """Compile every kernel source and link libmlra.so, and the launch module;
+    returns the library's path."""
     if not force and not _stale():
         return LIB
     objdir = os.path.join(PKG, "_build")
@@ -51,6 +72,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
         objs.append(obj)
+    ext_obj = os.path.join(objdir, "launch_ext.o")
+    ext_tmp = EXT + f".tmp{os.getpid()}"
+    ext_compile, ext_link = _ext_commands(ext_obj, ext_tmp)
+    procs.append((ext_compile[-3], subprocess.Popen(ext_compile, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -66,6 +91,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         print(" ".join(link), flush=True)
     subprocess.run(link, check=True)
     os.replace(tmp, LIB)
+    subprocess.run(ext_link, check=True)
+    os.replace(ext_tmp, EXT)
     return LIB
 
 

@@ -18,7 +18,7 @@
 //                S[slot] = Q C^T + Qr Kr^T   K = d_c + d_r, N = KT
 //                O += P[slot] C              P from TMEM, the same tile of C as
 //                                            MN-major operand, N = VN
-//   others     softmax, one thread per row (a TMEM lane): one pass with a
+//   warps 4..  softmax, one thread per row (a TMEM lane): one pass with a
 //              running maximum and sum; P goes to TMEM as bf16 over the
 //              scores it came from; at the end O / sum is written
 // Two score slots keep the tensor pipe busy while a softmax runs: the two
@@ -74,12 +74,21 @@ struct Cfg {
     static constexpr int S_COLS = KT;
     static constexpr int O_COL = MT == 2 ? 256 : 2 * S_COLS;
     static constexpr int TMEM_COLS = O_COL + MT * VN <= 256 ? 256 : 512;
+    // the next scores' tile is waited for ahead of the PV before it, where its
+    // copy does not itself wait for that PV
+    static constexpr bool EARLY = MT == 2 || NC >= 3;
     static constexpr int SOFT_WARPS = 4 * MT;
-    static constexpr int THREADS = 64 + 32 * SOFT_WARPS;
+    static constexpr int THREADS = 128 + 32 * SOFT_WARPS;
     static_assert(NC >= 2 && SMEM <= kSmemMax, "shared memory");
     static_assert(O_COL + MT * VN <= 512, "TMEM");
     static_assert(Q_TILE % 1024 == 0 && C_CHUNK % 1024 == 0 && K_BYTES % 1024 == 0, "swizzle atoms stay aligned");
 };
+
+// Registers of the two softmax warpgroups (a row of 128 scores each thread)
+// and of the first warpgroup, out of what the block was launched with: 3 x 128
+// threads of at most 168.
+constexpr int kSoftRegs = 208, kOtherRegs = 80;
+static_assert(128 * (2 * kSoftRegs + kOtherRegs) <= 3 * 128 * 168, "the split fits the launch");
 
 struct Misc {
     uint64_t c_full[4], c_empty[4];
@@ -103,6 +112,36 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// Pairs of fp32 in one 64-bit register, for the packed FMA and add.
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) { return pack2(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+    uint32_t a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+    lo = __uint_as_float(a);
+    hi = __uint_as_float(b);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -213,6 +252,9 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
         const int32_t* bt = a.block_table + (size_t)n * a.max_pages;
         volatile int* abort_flag = &misc.abort_flag;
 
+        if constexpr (C::MT == 2) {
+            if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        }
         if (warp == 0) {
             // ------------------------------------------------------------ copies
             const int box = min(P, C::KT);
@@ -284,46 +326,54 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             const uint64_t dK = rope_desc<DR>(base + C::OFF_K);
             bool ok = mbar_wait_warp(&misc.q_full, 0);
             tc_fence_after();
+            // PV(w), then S(w + 2) = Q C^T + Qr Kr^T
             for (int w = -2; w < nitems && ok; ++w) {
+                const int u = w + 2, ui = u / C::MT, um = u % C::MT, ucs = ui % C::NC, uks = ui % C::NK;
+                const bool more = u < nitems;
+                auto tile_landed = [&]() {
+                    return !more || um != 0 ||
+                           (mbar_wait_warp(&misc.k_full[uks], (ui / C::NK) & 1) && mbar_wait_warp(&misc.c_full[ucs], (ui / C::NC) & 1));
+                };
+                if (C::EARLY || w < 0) {
+                    ok = tile_landed();
+                    if (!ok) break;
+                }
                 if (w >= 0) {
-                    // O += P(w) C
                     const int i = w / C::MT, m = w % C::MT, cs = i % C::NC, slot = w & 1;
+                    const uint32_t d = tmem + C::O_COL + m * C::VN, p = tmem + slot * C::S_COLS;
+                    const uint64_t v = dV + ((cs * C::C_BYTES) >> 4);
                     ok = mbar_wait_warp(&misc.p_full[slot], (w >> 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t d = tmem + C::O_COL + m * C::VN, p = tmem + slot * C::S_COLS;
-                    const uint64_t v = dV + ((cs * C::C_BYTES) >> 4);
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < C::KT / 16; ++k) mma_bf16_ts(d, p + 8 * k, v + (k * 2048 >> 4), ID_O, (i | k) ? 1u : 0u);
                         mma_commit(&misc.o_done[slot]);
                         if (m == C::MT - 1) mma_commit(&misc.c_empty[cs]);
                     }
-                    __syncwarp();
-                }
-                if (w + 2 < nitems) {
-                    // S(w + 2) = Q C^T + Qr Kr^T
-                    const int u = w + 2, i = u / C::MT, m = u % C::MT, cs = i % C::NC, ks = i % C::NK;
-                    if (m == 0) {
-                        ok = mbar_wait_warp(&misc.k_full[ks], (i / C::NK) & 1) && mbar_wait_warp(&misc.c_full[cs], (i / C::NC) & 1);
+                    if (!C::EARLY) {
+                        __syncwarp();
+                        ok = tile_landed();
                         if (!ok) break;
-                        tc_fence_after();
                     }
+                }
+                if (more) {
                     const uint32_t d = tmem + (u & 1) * C::S_COLS;
-                    const uint64_t q = dQ + ((m * C::Q_TILE) >> 4), c = dC + ((cs * C::C_BYTES) >> 4);
+                    const uint64_t q = dQ + ((um * C::Q_TILE) >> 4), c = dC + ((ucs * C::C_BYTES) >> 4);
+                    tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < DR / 16; ++k)
-                            mma_bf16(d, dQr + ((m * C::Q_TILE) >> 4) + 2 * k, dK + ((ks * C::K_BYTES) >> 4) + 2 * k, ID_S, k ? 1u : 0u);
+                            mma_bf16(d, dQr + ((um * C::Q_TILE) >> 4) + 2 * k, dK + ((uks * C::K_BYTES) >> 4) + 2 * k, ID_S, k ? 1u : 0u);
 #pragma unroll
                         for (int k = 0; k < DC / 16; ++k)
                             mma_bf16(d, q + ((k / 4 * C::Q_CHUNK) >> 4) + k % 4 * 2, c + ((k / 4 * C::C_CHUNK) >> 4) + k % 4 * 2, ID_S, 1u);
                         mma_commit(&misc.s_full[u & 1]);
-                        if (m == C::MT - 1) mma_commit(&misc.k_empty[ks]);
+                        if (um == C::MT - 1) mma_commit(&misc.k_empty[uks]);
                     }
-                    __syncwarp();
                 }
-                if (__shfl_sync(0xffffffffu, *abort_flag, 0)) ok = false;
+                __syncwarp();
+                if ((w & 7) == 0 && __shfl_sync(0xffffffffu, *abort_flag, 0)) ok = false;
             }
             if (!ok && lane == 0) *abort_flag = 1;
             // every MMA has finished before TMEM is freed
@@ -331,9 +381,10 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             __syncwarp();
             mbar_wait(&misc.drain, 0, 200000000ull);
             __syncwarp();
-        } else {
+        } else if (warp >= 4) {
             // ------------------------------------------------------------ softmax
-            const int g = (warp - 2) / 4;                 // row tile (MT = 2) of this warpgroup
+            if constexpr (C::MT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+            const int g = (warp - 4) / 4;                 // row tile (MT = 2) of this warpgroup
             const int quad = warp & 3;                    // TMEM lane quadrant
             const int r = quad * 32 + lane;               // row within the 128
             const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
@@ -346,7 +397,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             {
                 // every page of the sequence has to lie in the pool
                 bool bad = false;
-                for (int e = threadIdx.x - 64; e < ceil_div(L, P); e += 32 * C::SOFT_WARPS) {
+                for (int e = threadIdx.x - 128; e < ceil_div(L, P); e += 32 * C::SOFT_WARPS) {
                     const int page = __ldg(bt + e);
                     bad |= page < 0 || page >= a.num_pages;
                 }
@@ -375,17 +426,23 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                     for (int j = 0; j < C::KT; ++j) x[j] = j > limit ? none : x[j];
                 }
                 // the largest scaled score (the smallest raw one under a negative scale)
-                float top[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) top[k] = __uint_as_float(x[k]);
+                float top[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
                 if (sc < 0.f) {
 #pragma unroll
-                    for (int j = 4; j < C::KT; ++j) top[j & 3] = fminf(top[j & 3], __uint_as_float(x[j]));
-                    top[0] = fminf(fminf(top[0], top[1]), fminf(top[2], top[3])) * sc;
+                    for (int j = 2; j < C::KT; j += 2) {
+                        top[0] = fminf(top[0], __uint_as_float(x[j]));
+                        top[1] = fminf(top[1], __uint_as_float(x[j + 1]));
+                    }
+                    top[0] = fminf(top[0], top[1]) * sc;
                 } else {
+                    top[0] = fmaxf(top[0], top[1]);
+                    top[1] = fmaxf(__uint_as_float(x[2]), __uint_as_float(x[3]));
 #pragma unroll
-                    for (int j = 4; j < C::KT; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(x[j]));
-                    top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
+                    for (int j = 4; j < C::KT; j += 4) {
+                        top[0] = max3(top[0], __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+                        top[1] = max3(top[1], __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
+                    }
+                    top[0] = fmaxf(top[0], top[1]) * sc;
                 }
                 if (i == 0) {
                     mx = top[0];  // token 0 is seen by every row
@@ -413,22 +470,6 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                         tmem_wait_st();
                     }
                 }
-                float sum[2] = {0.f, 0.f};
-#pragma unroll
-                for (int j = 0; j < C::KT; j += 2) {
-                    float p0 = ex2(fmaf(__uint_as_float(x[j]), sc, -mx)), p1 = ex2(fmaf(__uint_as_float(x[j + 1]), sc, -mx));
-                    if (diagonal) p0 = j > limit ? 0.f : p0, p1 = j + 1 > limit ? 0.f : p1;
-                    sum[0] += p0;
-                    sum[1] += p1;
-                    x[j / 2] = pack_bf16(p0, p1);
-                }
-                l += sum[0] + sum[1];
-                if constexpr (C::KT == 32) {
-                    tmem_st16(s_addr, x);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < C::KT / 64; ++c) tmem_st32(s_addr + 32 * c, x + 32 * c);
-                }
                 // slots behind the last token (stale, or another sequence's) become
                 // zero before the output MMA reads them: 0 * NaN is NaN
                 if (tok0 + C::KT > kv_end) {
@@ -439,10 +480,31 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                             make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
                 }
+                const uint64_t sc2 = pack2(sc, sc), mx2 = pack2(-mx, -mx);
+                uint64_t sum[2] = {0, 0};
+#pragma unroll
+                for (int j = 0; j < C::KT; j += 2) {
+                    float p0, p1;
+                    unpack2(fma2(pack2(x[j], x[j + 1]), sc2, mx2), p0, p1);
+                    p0 = ex2(p0);
+                    p1 = ex2(p1);
+                    if (diagonal) p0 = j > limit ? 0.f : p0, p1 = j + 1 > limit ? 0.f : p1;
+                    sum[j / 2 & 1] = add2(sum[j / 2 & 1], pack2(p0, p1));
+                    x[j / 2] = pack_bf16(p0, p1);
+                }
+                if constexpr (C::KT == 32) {
+                    tmem_st16(s_addr, x);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < C::KT / 64; ++c) tmem_st32(s_addr + 32 * c, x + 32 * c);
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&misc.p_full[slot]);
+                float s0, s1;
+                unpack2(add2(sum[0], sum[1]), s0, s1);
+                l += s0 + s1;
             }
             if (ok) {
                 const int v = w - C::MT;  // this tile's last item
@@ -455,7 +517,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             }
             named_bar_sync<1, 32 * C::SOFT_WARPS>();  // every page check is in
             const bool bad = misc.bad != 0 || !ok;
-            if (misc.bad != 0 && threadIdx.x == 64 && a.status != nullptr) record_error(a.status, MLRA_ERR_DEVICE_BAD_INDEX);
+            if (misc.bad != 0 && threadIdx.x == 128 && a.status != nullptr) record_error(a.status, MLRA_ERR_DEVICE_BAD_INDEX);
             const float inv = a.out_scale / l;
             __nv_bfloat16* dst = a.out + (out0 + g * 128 + r) * W + b * DC + v0;
 #pragma unroll 1
@@ -496,6 +558,15 @@ cudaError_t launch_cfg(const PrefillArgs& a, cudaStream_t stream) {
     auto kernel = prefill_kernel<DC, DR>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
+    if constexpr (C::MT == 2) {
+        // the softmax warps' registers come out of what the block is launched
+        // with; a build that allots less must not launch (they would wait forever)
+        static const int regs = [&] {
+            cudaFuncAttributes at;
+            return cudaFuncGetAttributes(&at, kernel) == cudaSuccess ? at.numRegs : 0;
+        }();
+        if (regs / 8 * 8 * C::THREADS < 128 * (2 * kSoftRegs + kOtherRegs)) return cudaErrorInvalidConfiguration;
+    }
     const long long places = (long long)(q_rows / C::BM) + a.batch;
     const long long grid = places * a.branches * C::NV;
     if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;

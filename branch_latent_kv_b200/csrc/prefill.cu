@@ -87,7 +87,7 @@ struct Cfg {
 // Registers of the two softmax warpgroups (a row of 128 scores each thread)
 // and of the first warpgroup, out of what the block was launched with: 3 x 128
 // threads of at most 168.
-constexpr int kSoftRegs = 208, kOtherRegs = 80;
+constexpr int kSoftRegs = 200, kOtherRegs = 104;
 static_assert(128 * (2 * kSoftRegs + kOtherRegs) <= 3 * 128 * 168, "the split fits the launch");
 
 struct Misc {
@@ -95,7 +95,8 @@ struct Misc {
     uint64_t k_full[4], k_empty[4];
     uint64_t s_full[2];   // item w in slot w % 2: its scores are in TMEM
     uint64_t p_full[2];   // its probabilities are in TMEM
-    uint64_t o_done[2];   // its output MMA has finished
+    uint64_t o_done[2];   // its output MMA has finished (MT = 2: the last item's only, as s_full of
+                          // item w + 2 says so of the others: its MMAs come after PV(w))
     uint64_t q_full;
     uint64_t drain;
     uint32_t tmem_base;
@@ -324,56 +325,80 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             const uint64_t dC = smem_desc(base + C::OFF_C, 16, 1024, kLayoutSw128);           // K-major
             const uint64_t dV = smem_desc(base + C::OFF_C + v0 / 64 * C::C_CHUNK, C::C_CHUNK, 1024, kLayoutSw128);  // MN-major
             const uint64_t dK = rope_desc<DR>(base + C::OFF_K);
+            // (one warp's dependent instructions take four cycles and more each:
+            // ring positions are counted, not divided, and the two tiles unrolled)
+            struct Ring {
+                uint32_t at = 0, phase = 0;
+                __device__ __forceinline__ void next(uint32_t depth) {
+                    if (++at == depth) at = 0, phase ^= 1;
+                }
+            };
+            Ring c_new, k_new, c_old;  // the tile of the next scores (latents, keys); the tile of the next PV
+            auto landed = [&]() { return mbar_wait_warp(&misc.k_full[k_new.at], k_new.phase) && mbar_wait_warp(&misc.c_full[c_new.at], c_new.phase); };
+            auto scores = [&](int m, int slot) {  // the elected thread: S[slot] = Q C^T + Qr Kr^T of the new tile
+                const uint32_t d = tmem + slot * C::S_COLS;
+                const uint64_t qr = dQr + ((m * C::Q_TILE) >> 4), k0 = dK + ((k_new.at * C::K_BYTES) >> 4);
+                const uint64_t q = dQ + ((m * C::Q_TILE) >> 4), c = dC + ((c_new.at * C::C_BYTES) >> 4);
+#pragma unroll
+                for (int k = 0; k < DR / 16; ++k) mma_bf16(d, qr + 2 * k, k0 + 2 * k, ID_S, k ? 1u : 0u);
+#pragma unroll
+                for (int k = 0; k < DC / 16; ++k)
+                    mma_bf16(d, q + ((k / 4 * C::Q_CHUNK) >> 4) + k % 4 * 2, c + ((k / 4 * C::C_CHUNK) >> 4) + k % 4 * 2, ID_S, 1u);
+                mma_commit(&misc.s_full[slot]);
+                if (m == C::MT - 1) mma_commit(&misc.k_empty[k_new.at]);
+            };
+            auto values = [&](int m, int slot, bool first, bool last) {  // the elected thread: O[m] += P[slot] C of the old tile
+                const uint32_t d = tmem + C::O_COL + m * C::VN, p = tmem + slot * C::S_COLS;
+                const uint64_t v = dV + ((c_old.at * C::C_BYTES) >> 4);
+#pragma unroll
+                for (int k = 0; k < C::KT / 16; ++k) mma_bf16_ts(d, p + 8 * k, v + (k * 2048 >> 4), ID_O, k == 0 && first ? 0u : 1u);
+                if (C::MT == 1 || last) mma_commit(&misc.o_done[slot]);
+                if (m == C::MT - 1) mma_commit(&misc.c_empty[c_old.at]);
+            };
             bool ok = mbar_wait_warp(&misc.q_full, 0);
-            tc_fence_after();
-            // PV(w), then S(w + 2) = Q C^T + Qr Kr^T
-            for (int w = -2; w < nitems && ok; ++w) {
-                const int u = w + 2, ui = u / C::MT, um = u % C::MT, ucs = ui % C::NC, uks = ui % C::NK;
-                const bool more = u < nitems;
-                auto tile_landed = [&]() {
-                    return !more || um != 0 ||
-                           (mbar_wait_warp(&misc.k_full[uks], (ui / C::NK) & 1) && mbar_wait_warp(&misc.c_full[ucs], (ui / C::NC) & 1));
-                };
-                if (C::EARLY || w < 0) {
-                    ok = tile_landed();
-                    if (!ok) break;
+            // the first scores: of both row tiles, or of the first two token tiles
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (s == 0 || C::MT == 1) ok = ok && s < ntiles && landed();
+                if (s > 0 && C::MT == 1 && s >= ntiles) ok = true;  // (one tile only)
+                else if (ok) {
+                    tc_fence_after();
+                    if (elect_one()) scores(C::MT == 2 ? s : 0, s);
+                    __syncwarp();
+                    if (s == C::MT - 1 || C::MT == 1) c_new.next(C::NC), k_new.next(C::NK);
                 }
-                if (w >= 0) {
-                    const int i = w / C::MT, m = w % C::MT, cs = i % C::NC, slot = w & 1;
-                    const uint32_t d = tmem + C::O_COL + m * C::VN, p = tmem + slot * C::S_COLS;
-                    const uint64_t v = dV + ((cs * C::C_BYTES) >> 4);
-                    ok = mbar_wait_warp(&misc.p_full[slot], (w >> 1) & 1);
+            }
+            // (the next scores' tile is waited for before the probabilities where its
+            // copy cannot depend on the PV about to be issued, else after that)
+            for (int i = 0; i < ntiles && ok; ++i) {
+                const bool more = i + (C::MT == 2 ? 1 : 2) < ntiles;
+                if (C::EARLY && more) ok = landed();
+#pragma unroll
+                for (int m = 0; m < C::MT; ++m) {
+                    const int slot = C::MT == 2 ? m : i & 1;
+                    ok = ok && mbar_wait_warp(&misc.p_full[slot], (C::MT == 2 ? i : i >> 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < C::KT / 16; ++k) mma_bf16_ts(d, p + 8 * k, v + (k * 2048 >> 4), ID_O, (i | k) ? 1u : 0u);
-                        mma_commit(&misc.o_done[slot]);
-                        if (m == C::MT - 1) mma_commit(&misc.c_empty[cs]);
-                    }
-                    if (!C::EARLY) {
+                    if constexpr (C::EARLY) {
+                        if (elect_one()) {
+                            values(m, slot, i == 0, i == ntiles - 1);
+                            if (more) scores(m, slot);
+                        }
                         __syncwarp();
-                        ok = tile_landed();
+                    } else {
+                        if (elect_one()) values(m, slot, i == 0, i == ntiles - 1);
+                        __syncwarp();
+                        ok = !more || landed();
                         if (!ok) break;
+                        tc_fence_after();
+                        if (more && elect_one()) scores(m, slot);
+                        __syncwarp();
                     }
                 }
-                if (more) {
-                    const uint32_t d = tmem + (u & 1) * C::S_COLS;
-                    const uint64_t q = dQ + ((um * C::Q_TILE) >> 4), c = dC + ((ucs * C::C_BYTES) >> 4);
-                    tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < DR / 16; ++k)
-                            mma_bf16(d, dQr + ((um * C::Q_TILE) >> 4) + 2 * k, dK + ((uks * C::K_BYTES) >> 4) + 2 * k, ID_S, k ? 1u : 0u);
-#pragma unroll
-                        for (int k = 0; k < DC / 16; ++k)
-                            mma_bf16(d, q + ((k / 4 * C::Q_CHUNK) >> 4) + k % 4 * 2, c + ((k / 4 * C::C_CHUNK) >> 4) + k % 4 * 2, ID_S, 1u);
-                        mma_commit(&misc.s_full[u & 1]);
-                        if (um == C::MT - 1) mma_commit(&misc.k_empty[uks]);
-                    }
-                }
-                __syncwarp();
-                if ((w & 7) == 0 && __shfl_sync(0xffffffffu, *abort_flag, 0)) ok = false;
+                c_old.next(C::NC);
+                c_new.next(C::NC);
+                k_new.next(C::NK);
+                if ((i & 7) == 7 && __shfl_sync(0xffffffffu, *abort_flag, 0)) ok = false;
             }
             if (!ok && lane == 0) *abort_flag = 1;
             // every MMA has finished before TMEM is freed
@@ -392,7 +417,9 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             const int row = row0 + g * 128 + r;
             const int pos = past + min(row, rows - 1) / H;  // last token of this row
             const int pos_first = past + min(row0 + g * 128 + quad * 32, rows - 1) / H;  // of the warp's first row
-            const float sc = a.scale_log2;
+            // (a scale of 0 as 1e-30: every finite score still weighs the same, and a
+            // masked score, infinite, stays so)
+            const float sc = a.scale_log2 == 0.f ? 1e-30f : a.scale_log2;
             const int L = past + rows / H;
             {
                 // every page of the sequence has to lie in the pool
@@ -419,30 +446,27 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                 reg_tie<C::KT>(x);
                 // tokens j > limit of the tile are masked (a whole warp's rows at once see it all otherwise)
                 const int limit = pos - tok0;
-                const bool diagonal = pos_first - tok0 < C::KT - 1;
-                if (diagonal) {
+                if (pos_first - tok0 < C::KT - 1) {
                     const uint32_t none = sc < 0.f ? 0x7f800000u : 0xff800000u;
 #pragma unroll
                     for (int j = 0; j < C::KT; ++j) x[j] = j > limit ? none : x[j];
                 }
                 // the largest scaled score (the smallest raw one under a negative scale)
-                float top[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
+                float top[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top[k] = __uint_as_float(x[k]);
                 if (sc < 0.f) {
 #pragma unroll
-                    for (int j = 2; j < C::KT; j += 2) {
-                        top[0] = fminf(top[0], __uint_as_float(x[j]));
-                        top[1] = fminf(top[1], __uint_as_float(x[j + 1]));
-                    }
-                    top[0] = fminf(top[0], top[1]) * sc;
+                    for (int j = 4; j < C::KT; ++j) top[j & 3] = fminf(top[j & 3], __uint_as_float(x[j]));
+                    top[0] = fminf(fminf(top[0], top[1]), fminf(top[2], top[3])) * sc;
                 } else {
-                    top[0] = fmaxf(top[0], top[1]);
-                    top[1] = fmaxf(__uint_as_float(x[2]), __uint_as_float(x[3]));
 #pragma unroll
-                    for (int j = 4; j < C::KT; j += 4) {
-                        top[0] = max3(top[0], __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
-                        top[1] = max3(top[1], __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
-                    }
-                    top[0] = fmaxf(top[0], top[1]) * sc;
+                    for (int j = 4; j + 8 <= C::KT; j += 8)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) top[k] = max3(top[k], __uint_as_float(x[j + 2 * k]), __uint_as_float(x[j + 2 * k + 1]));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], __uint_as_float(x[C::KT - 4 + k]));
+                    top[0] = fmaxf(max3(top[0], top[1], top[2]), top[3]) * sc;
                 }
                 if (i == 0) {
                     mx = top[0];  // token 0 is seen by every row
@@ -450,10 +474,11 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                     const bool grow = top[0] > mx + kRescale;
                     if (__any_sync(0xffffffffu, grow)) {
                         // O of this warp's rows at the new maximum, once the PV before is done
-                        const int v = w - C::MT;
-                        ok = mbar_wait_warp(&misc.o_done[v & 1], (v >> 1) & 1);
-                        if (!ok) break;
-                        tc_fence_after();
+                        if constexpr (C::MT == 1) {
+                            ok = mbar_wait_warp(&misc.o_done[(w - 1) & 1], ((w - 1) >> 1) & 1);
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
                         const float alpha = grow ? ex2(mx - top[0]) : 1.f;
                         if (grow) mx = top[0];
                         l *= alpha;
@@ -488,7 +513,6 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                     unpack2(fma2(pack2(x[j], x[j + 1]), sc2, mx2), p0, p1);
                     p0 = ex2(p0);
                     p1 = ex2(p1);
-                    if (diagonal) p0 = j > limit ? 0.f : p0, p1 = j + 1 > limit ? 0.f : p1;
                     sum[j / 2 & 1] = add2(sum[j / 2 & 1], pack2(p0, p1));
                     x[j / 2] = pack_bf16(p0, p1);
                 }
@@ -508,7 +532,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             }
             if (ok) {
                 const int v = w - C::MT;  // this tile's last item
-                ok = mbar_wait_warp(&misc.o_done[v & 1], (v >> 1) & 1);
+                ok = mbar_wait_warp(&misc.o_done[v & 1], C::MT == 1 ? (v >> 1) & 1 : 0);
                 tc_fence_after();
             }
             if (!ok && lane == 0) {

@@ -47,39 +47,43 @@ constexpr float kRescale = 8.0f;  // log2 of how far a score may pass the runnin
 
 template <int DC, int DR>
 struct Cfg {
-    static constexpr int MT = DC <= 128 ? 2 : 1;                      // 128-row tiles per CTA
-    static constexpr int KT = DC <= 128 ? 128 : DC == 256 ? 64 : 32;  // tokens per tile
-    static constexpr int VN = DC <= 256 ? DC : 256;                   // value columns per CTA
-    static constexpr int NV = DC / VN;                                // CTAs per row block and branch
+    static constexpr bool PAIR = DC == 512;             // two CTAs share the columns of a row block
+    static constexpr int NV = PAIR ? 2 : 1;             // CTAs per row block and branch
+    static constexpr int DL = DC / NV;                  // latent columns of this CTA
+    static constexpr int RL = PAIR ? 32 : DR;           // RoPE columns of this CTA
+    static constexpr int MT = DL <= 128 ? 2 : 1;        // 128-row tiles per CTA
+    static constexpr int KT = DL <= 128 ? 128 : 64;     // tokens per tile
+    static constexpr int VN = DL;                       // value columns
     static constexpr int BM = 128 * MT;
-    static constexpr int NCH = DC / 64;  // 64-column (128-byte) chunks of a latent row
+    static constexpr int NCH = DL / 64;                 // 64-column (128-byte) chunks of a latent row
     static constexpr int Q_CHUNK = 128 * 128;
-    static constexpr int QR_BYTES = 128 * DR * 2;
+    static constexpr int QR_BYTES = 128 * RL * 2;
     static constexpr int Q_TILE = NCH * Q_CHUNK + QR_BYTES;
     static constexpr int C_CHUNK = KT * 128;
     static constexpr int C_BYTES = NCH * C_CHUNK;
-    static constexpr int K_BYTES = KT * DR * 2;
+    static constexpr int K_BYTES = KT * RL * 2;
+    static constexpr int X_BYTES = PAIR ? 128 * KT * 4 : 0;  // the other CTA's share of the scores
     static constexpr int MISC = 1024;
     // ring depths: the tile a PV reads, the one the next QK reads, and what
     // fits beyond
-    static constexpr int NK = DC == 64 ? 4 : DC == 256 ? 3 : 2;
-    static constexpr int NC_FIT = (kSmemMax - 1024 - MISC - MT * Q_TILE - NK * K_BYTES) / C_BYTES;
+    static constexpr int NK = DC == 64 ? 4 : DC >= 256 ? 3 : 2;
+    static constexpr int NC_FIT = (kSmemMax - 1024 - MISC - MT * Q_TILE - NK * K_BYTES - X_BYTES) / C_BYTES;
     static constexpr int NC = NC_FIT > 4 ? 4 : NC_FIT;
     static constexpr int OFF_Q = 0;  // Q tile m: chunks, then its RoPE part
     static constexpr int OFF_C = MT * Q_TILE;
     static constexpr int OFF_K = OFF_C + NC * C_BYTES;
-    static constexpr int OFF_MISC = OFF_K + NK * K_BYTES;
+    static constexpr int OFF_X = OFF_K + NK * K_BYTES;
+    static constexpr int OFF_MISC = OFF_X + X_BYTES;
     static constexpr int SMEM = OFF_MISC + MISC + 1024;
     // TMEM columns: two score slots, then the output tiles
     static constexpr int S_COLS = KT;
     static constexpr int O_COL = MT == 2 ? 256 : 2 * S_COLS;
     static constexpr int TMEM_COLS = O_COL + MT * VN <= 256 ? 256 : 512;
-    // the next scores' tile is waited for ahead of the PV before it, where its
-    // copy does not itself wait for that PV
-    static constexpr bool EARLY = MT == 2 || NC >= 3;
     static constexpr int SOFT_WARPS = 4 * MT;
     static constexpr int THREADS = 128 + 32 * SOFT_WARPS;
-    static_assert(NC >= 2 && SMEM <= kSmemMax, "shared memory");
+    // (the next scores' tile is waited for ahead of the PV before it, whose tile
+    // must not be the one that makes room for it)
+    static_assert((MT == 2 || NC >= 3) && NC >= 2 && SMEM <= kSmemMax, "shared memory");
     static_assert(O_COL + MT * VN <= 512, "TMEM");
     static_assert(Q_TILE % 1024 == 0 && C_CHUNK % 1024 == 0 && K_BYTES % 1024 == 0, "swizzle atoms stay aligned");
 };
@@ -97,6 +101,7 @@ struct Misc {
     uint64_t p_full[2];   // its probabilities are in TMEM
     uint64_t o_done[2];   // its output MMA has finished (MT = 2: the last item's only, as s_full of
                           // item w + 2 says so of the others: its MMAs come after PV(w))
+    uint64_t x_full, x_empty;  // a pair: the other CTA's scores of an item are here; it has read mine
     uint64_t q_full;
     uint64_t drain;
     uint32_t tmem_base;
@@ -186,7 +191,11 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
     Misc& misc = *reinterpret_cast<Misc*>(sm + C::OFF_MISC);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int H = a.heads, B = a.branches, P = a.page_size;
-    const int part = blockIdx.x % (B * C::NV), b = part / C::NV, v0 = part % C::NV * C::VN;
+    const int part = blockIdx.x % (B * C::NV), b = part / C::NV;
+    const int rank = part % C::NV;       // place in the pair (its cluster rank)
+    const int col0 = b * DC + rank * C::DL;  // this CTA's first column of a latent row
+    const bool has_rope = !C::PAIR || DR == 64 || rank == 0;
+    const int rope0 = C::PAIR && DR == 64 ? rank * C::RL : 0;  // its first RoPE column
     // a sequence's later row blocks see more tokens: they start first
     const long long place = places - 1 - blockIdx.x / (B * C::NV);
 
@@ -199,6 +208,8 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             mbar_init(&misc.p_full[i], 4);
             mbar_init(&misc.o_done[i], 1);
         }
+        mbar_init(&misc.x_full, 1);
+        mbar_init(&misc.x_empty, 4);
         mbar_init(&misc.q_full, 1);
         mbar_init(&misc.drain, 1);
         misc.abort_flag = 0;
@@ -228,7 +239,8 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
         }
     }
     tc_fence_before();
-    __syncthreads();
+    if constexpr (C::PAIR) cluster_sync();  // (the other CTA's barriers are set up too)
+    else __syncthreads();
     tc_fence_after();
     const int n = misc.job[0], row0 = misc.job[1], rows = misc.job[2], past = misc.job[4];
     const size_t out0 = (size_t)misc.job[3] + row0;  // this CTA's first (token, head) row of out
@@ -244,7 +256,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
     if (n >= 0 && past < 0) {  // a bad length: zeros
         const int left = min(C::BM, rows - row0);
         for (int e = threadIdx.x; e < left * (C::VN / 8); e += C::THREADS)
-            *reinterpret_cast<uint4*>(a.out + (out0 + e / (C::VN / 8)) * W + b * DC + v0 + e % (C::VN / 8) * 8) =
+            *reinterpret_cast<uint4*>(a.out + (out0 + e / (C::VN / 8)) * W + col0 + e % (C::VN / 8) * 8) =
                 make_uint4(0u, 0u, 0u, 0u);
     } else if (n >= 0) {
         const int last_row = min(row0 + C::BM, rows) - 1;
@@ -261,13 +273,13 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             const int box = min(P, C::KT);
             bool ok = true;
             if (lane == 0) {
-                mbar_arrive_expect_tx(&misc.q_full, C::MT * C::Q_TILE);
+                mbar_arrive_expect_tx(&misc.q_full, C::MT * (C::NCH * C::Q_CHUNK + (has_rope ? C::QR_BYTES : 0)));
                 for (int m = 0; m < C::MT; ++m) {
                     uint8_t* dst = sm + C::OFF_Q + m * C::Q_TILE;
                     const int y = (int)out0 + m * 128;
                     for (int c = 0; c < C::NCH; ++c)
-                        tma_load_2d(dst + c * C::Q_CHUNK, &maps.q, b * DC + c * 64, y, &misc.q_full);
-                    tma_load_2d(dst + C::NCH * C::Q_CHUNK, &maps.qr, 0, y, &misc.q_full);
+                        tma_load_2d(dst + c * C::Q_CHUNK, &maps.q, col0 + c * 64, y, &misc.q_full);
+                    if (has_rope) tma_load_2d(dst + C::NCH * C::Q_CHUNK, &maps.qr, rope0, y, &misc.q_full);
                 }
             }
             int win = 0, page_of_lane = 0;  // 32 block-table entries from `win` on
@@ -286,7 +298,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                     if (ok && i >= C::NC) ok = mbar_wait(&misc.c_empty[cs], (i / C::NC - 1) & 1);
                     ok = ok && !*abort_flag;
                     if (ok) {
-                        mbar_arrive_expect_tx(&misc.k_full[ks], nbox * box * DR * 2);
+                        mbar_arrive_expect_tx(&misc.k_full[ks], has_rope ? nbox * box * C::RL * 2 : 0);
                         mbar_arrive_expect_tx(&misc.c_full[cs], nbox * box * C::NCH * 128);
                     }
                 }
@@ -298,10 +310,11 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                     page = page >= 0 && page < a.num_pages ? page : 0;  // (the softmax warps report it)
                     const int y = page * P + tok % P;
                     if (lane == 0) {
-                        tma_load_2d(sm + C::OFF_K + ks * C::K_BYTES + q * box * DR * 2, &maps.rope, 0, y, &misc.k_full[ks]);
+                        if (has_rope)
+                            tma_load_2d(sm + C::OFF_K + ks * C::K_BYTES + q * box * C::RL * 2, &maps.rope, rope0, y, &misc.k_full[ks]);
                         for (int c = 0; c < C::NCH; ++c)
                             tma_load_2d(sm + C::OFF_C + cs * C::C_BYTES + c * C::C_CHUNK + q * box * 128, &maps.lat,
-                                        b * DC + c * 64, y, &misc.c_full[cs]);
+                                        col0 + c * 64, y, &misc.c_full[cs]);
                     }
                 }
                 done = i + 1;
@@ -321,10 +334,10 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             constexpr uint32_t ID_O = idesc_bf16_f32(128, C::VN, false, true);
             const uint32_t base = smem_u32(sm);
             const uint64_t dQ = smem_desc(base + C::OFF_Q, 16, 1024, kLayoutSw128);
-            const uint64_t dQr = rope_desc<DR>(base + C::OFF_Q + C::NCH * C::Q_CHUNK);
+            const uint64_t dQr = rope_desc<C::RL>(base + C::OFF_Q + C::NCH * C::Q_CHUNK);
             const uint64_t dC = smem_desc(base + C::OFF_C, 16, 1024, kLayoutSw128);           // K-major
-            const uint64_t dV = smem_desc(base + C::OFF_C + v0 / 64 * C::C_CHUNK, C::C_CHUNK, 1024, kLayoutSw128);  // MN-major
-            const uint64_t dK = rope_desc<DR>(base + C::OFF_K);
+            const uint64_t dV = smem_desc(base + C::OFF_C, C::C_CHUNK, 1024, kLayoutSw128);  // MN-major
+            const uint64_t dK = rope_desc<C::RL>(base + C::OFF_K);
             // (one warp's dependent instructions take four cycles and more each:
             // ring positions are counted, not divided, and the two tiles unrolled)
             struct Ring {
@@ -340,10 +353,12 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                 const uint64_t qr = dQr + ((m * C::Q_TILE) >> 4), k0 = dK + ((k_new.at * C::K_BYTES) >> 4);
                 const uint64_t q = dQ + ((m * C::Q_TILE) >> 4), c = dC + ((c_new.at * C::C_BYTES) >> 4);
 #pragma unroll
-                for (int k = 0; k < DR / 16; ++k) mma_bf16(d, qr + 2 * k, k0 + 2 * k, ID_S, k ? 1u : 0u);
+                for (int k = 0; k < C::RL / 16; ++k)
+                    if (has_rope) mma_bf16(d, qr + 2 * k, k0 + 2 * k, ID_S, k ? 1u : 0u);
 #pragma unroll
-                for (int k = 0; k < DC / 16; ++k)
-                    mma_bf16(d, q + ((k / 4 * C::Q_CHUNK) >> 4) + k % 4 * 2, c + ((k / 4 * C::C_CHUNK) >> 4) + k % 4 * 2, ID_S, 1u);
+                for (int k = 0; k < C::DL / 16; ++k)
+                    mma_bf16(d, q + ((k / 4 * C::Q_CHUNK) >> 4) + k % 4 * 2, c + ((k / 4 * C::C_CHUNK) >> 4) + k % 4 * 2, ID_S,
+                             k || has_rope ? 1u : 0u);
                 mma_commit(&misc.s_full[slot]);
                 if (m == C::MT - 1) mma_commit(&misc.k_empty[k_new.at]);
             };
@@ -368,32 +383,20 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                     if (s == C::MT - 1 || C::MT == 1) c_new.next(C::NC), k_new.next(C::NK);
                 }
             }
-            // (the next scores' tile is waited for before the probabilities where its
-            // copy cannot depend on the PV about to be issued, else after that)
             for (int i = 0; i < ntiles && ok; ++i) {
                 const bool more = i + (C::MT == 2 ? 1 : 2) < ntiles;
-                if (C::EARLY && more) ok = landed();
+                if (more) ok = landed();
 #pragma unroll
                 for (int m = 0; m < C::MT; ++m) {
                     const int slot = C::MT == 2 ? m : i & 1;
                     ok = ok && mbar_wait_warp(&misc.p_full[slot], (C::MT == 2 ? i : i >> 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    if constexpr (C::EARLY) {
-                        if (elect_one()) {
-                            values(m, slot, i == 0, i == ntiles - 1);
-                            if (more) scores(m, slot);
-                        }
-                        __syncwarp();
-                    } else {
-                        if (elect_one()) values(m, slot, i == 0, i == ntiles - 1);
-                        __syncwarp();
-                        ok = !more || landed();
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (more && elect_one()) scores(m, slot);
-                        __syncwarp();
+                    if (elect_one()) {
+                        values(m, slot, i == 0, i == ntiles - 1);
+                        if (more) scores(m, slot);
                     }
+                    __syncwarp();
                 }
                 c_old.next(C::NC);
                 c_new.next(C::NC);
@@ -444,6 +447,32 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                 for (int c = 0; c < C::KT / 32; ++c) tmem_ld32(s_addr + 32 * c, x + 32 * c);
                 tmem_wait_ld();
                 reg_tie<C::KT>(x);
+                if constexpr (C::PAIR) {
+                    // the scores of the other CTA's columns: each thread sends its row's share
+                    // to the same thread there, [four tokens][row] of 16 bytes, and adds what
+                    // it gets (a sum of two, so both CTAs have the same bits)
+                    float4* here = reinterpret_cast<float4*>(sm + C::OFF_X) + r;
+                    const uint32_t there = map_shared_rank(smem_u32(here), rank ^ 1);
+                    const uint32_t full = map_shared_rank(smem_u32(&misc.x_full), rank ^ 1);
+                    if (r == 0) mbar_arrive_expect_tx(&misc.x_full, C::X_BYTES);
+                    if (w > 0) ok = mbar_wait_warp(&misc.x_empty, (w - 1) & 1);
+                    if (!ok) break;
+#pragma unroll
+                    for (int c = 0; c < C::KT / 4; ++c)
+                        st_async_v4(there + c * 2048, full, x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+                    ok = mbar_wait_warp(&misc.x_full, w & 1);
+                    if (!ok) break;
+#pragma unroll
+                    for (int c = 0; c < C::KT / 4; ++c) {
+                        const float4 v = here[c * 128];
+                        x[4 * c] = __float_as_uint(__uint_as_float(x[4 * c]) + v.x);
+                        x[4 * c + 1] = __float_as_uint(__uint_as_float(x[4 * c + 1]) + v.y);
+                        x[4 * c + 2] = __float_as_uint(__uint_as_float(x[4 * c + 2]) + v.z);
+                        x[4 * c + 3] = __float_as_uint(__uint_as_float(x[4 * c + 3]) + v.w);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(map_shared_rank(smem_u32(&misc.x_empty), rank ^ 1));
+                }
                 // tokens j > limit of the tile are masked (a whole warp's rows at once see it all otherwise)
                 const int limit = pos - tok0;
                 if (pos_first - tok0 < C::KT - 1) {
@@ -516,12 +545,8 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                     sum[j / 2 & 1] = add2(sum[j / 2 & 1], pack2(p0, p1));
                     x[j / 2] = pack_bf16(p0, p1);
                 }
-                if constexpr (C::KT == 32) {
-                    tmem_st16(s_addr, x);
-                } else {
 #pragma unroll
-                    for (int c = 0; c < C::KT / 64; ++c) tmem_st32(s_addr + 32 * c, x + 32 * c);
-                }
+                for (int c = 0; c < C::KT / 64; ++c) tmem_st32(s_addr + 32 * c, x + 32 * c);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -543,7 +568,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             const bool bad = misc.bad != 0 || !ok;
             if (misc.bad != 0 && threadIdx.x == 128 && a.status != nullptr) record_error(a.status, MLRA_ERR_DEVICE_BAD_INDEX);
             const float inv = a.out_scale / l;
-            __nv_bfloat16* dst = a.out + (out0 + g * 128 + r) * W + b * DC + v0;
+            __nv_bfloat16* dst = a.out + (out0 + g * 128 + r) * W + col0;
 #pragma unroll 1
             for (int c = 0; c < C::VN / 32; ++c) {
                 uint32_t o[32];
@@ -562,7 +587,8 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             tc_fence_before();
         }
     }
-    __syncthreads();
+    if constexpr (C::PAIR) cluster_sync();  // (nothing of this CTA's memory is written any more)
+    else __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
 }
@@ -575,9 +601,9 @@ cudaError_t launch_cfg(const PrefillArgs& a, cudaStream_t stream) {
     const uint64_t rows = (uint64_t)a.num_pages * a.page_size;
     const uint32_t box = a.page_size < C::KT ? a.page_size : C::KT;
     if (!encode_rows(&maps.q, a.q_lat, 2, W, q_rows, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_rows(&maps.qr, a.q_rope, 2, DR, q_rows, DR, 128, rope_swizzle(DR)) ||
+        !encode_rows(&maps.qr, a.q_rope, 2, DR, q_rows, C::RL, 128, rope_swizzle(C::RL)) ||
         !encode_rows(&maps.lat, a.latent, 2, W, rows, 64, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_rows(&maps.rope, a.rope, 2, DR, rows, DR, box, rope_swizzle(DR)))
+        !encode_rows(&maps.rope, a.rope, 2, DR, rows, C::RL, box, rope_swizzle(C::RL)))
         return cudaErrorInvalidValue;
     auto kernel = prefill_kernel<DC, DR>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
@@ -599,11 +625,13 @@ cudaError_t launch_cfg(const PrefillArgs& a, cudaStream_t stream) {
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {C::NV, 1, 1};
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = C::PAIR ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, maps, a, places);
 }
 

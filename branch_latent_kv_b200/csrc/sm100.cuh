@@ -444,6 +444,18 @@ __device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t addr) {
     return v;
 }
 
+// Arrives on a barrier of another CTA of the cluster (address from
+// map_shared_rank); what this thread read and wrote before is ordered before it.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote_bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
+}
+// Asynchronous 16-byte store to another CTA of the cluster, completing its 16
+// bytes on a barrier of that CTA (16-byte aligned; both from map_shared_rank).
+__device__ __forceinline__ void st_async_v4(uint32_t remote, uint32_t remote_bar, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%2, %3, %4, %5}, [%1];"
+                 ::"r"(remote), "r"(remote_bar), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
 // ---------------------------------------------------------------- named barriers
 // barrier.cta.red.or over `count` threads of named barrier `id`; every
 // participant gets the OR of all predicates.

@@ -58,33 +58,37 @@ struct Cfg {
     static constexpr int NCH = DL / 64;                 // 64-column (128-byte) chunks of a latent row
     static constexpr int Q_CHUNK = 128 * 128;
     static constexpr int QR_BYTES = 128 * RL * 2;
-    static constexpr int Q_TILE = NCH * Q_CHUNK + QR_BYTES;
+    static constexpr bool QT = MT == 1;                 // the latent queries live in TMEM, else in shared memory
+    static constexpr int Q_LAT = QT ? 0 : NCH * Q_CHUNK;
+    static constexpr int Q_TILE = Q_LAT + QR_BYTES;
     static constexpr int C_CHUNK = KT * 128;
     static constexpr int C_BYTES = NCH * C_CHUNK;
     static constexpr int K_BYTES = KT * RL * 2;
-    static constexpr int X_BYTES = PAIR ? 128 * KT * 4 : 0;  // the other CTA's share of the scores
+    static constexpr int X_BYTES = PAIR ? 128 * KT * 4 : 0;  // the other CTA's share of an item's scores (two slots)
     static constexpr int MISC = 1024;
     // ring depths: the tile a PV reads, the one the next QK reads, and what
     // fits beyond
     static constexpr int NK = DC == 64 ? 4 : DC >= 256 ? 3 : 2;
-    static constexpr int NC_FIT = (kSmemMax - 1024 - MISC - MT * Q_TILE - NK * K_BYTES - X_BYTES) / C_BYTES;
+    static constexpr int NC_FIT = (kSmemMax - 1024 - MISC - MT * Q_TILE - NK * K_BYTES - 2 * X_BYTES) / C_BYTES;
     static constexpr int NC = NC_FIT > 4 ? 4 : NC_FIT;
     static constexpr int OFF_Q = 0;  // Q tile m: chunks, then its RoPE part
     static constexpr int OFF_C = MT * Q_TILE;
     static constexpr int OFF_K = OFF_C + NC * C_BYTES;
     static constexpr int OFF_X = OFF_K + NK * K_BYTES;
-    static constexpr int OFF_MISC = OFF_X + X_BYTES;
+    static constexpr int OFF_MISC = OFF_X + 2 * X_BYTES;
     static constexpr int SMEM = OFF_MISC + MISC + 1024;
     // TMEM columns: two score slots, then the output tiles
     static constexpr int S_COLS = KT;
-    static constexpr int O_COL = MT == 2 ? 256 : 2 * S_COLS;
-    static constexpr int TMEM_COLS = O_COL + MT * VN <= 256 ? 256 : 512;
+    static constexpr int O_COL = 2 * S_COLS;
+    static constexpr int Q_COL = O_COL + MT * VN;       // QT: [rows][d_c / 2], pairs of bf16
+    static constexpr int COLS = Q_COL + (QT ? DL / 2 : 0);
+    static constexpr int TMEM_COLS = COLS <= 256 ? 256 : 512;
     static constexpr int SOFT_WARPS = 4 * MT;
-    static constexpr int THREADS = 128 + 32 * SOFT_WARPS;
+    static constexpr int THREADS = 128 + 32 * SOFT_WARPS + (PAIR ? 128 : 0);
     // (the next scores' tile is waited for ahead of the PV before it, whose tile
     // must not be the one that makes room for it)
     static_assert((MT == 2 || NC >= 3) && NC >= 2 && SMEM <= kSmemMax, "shared memory");
-    static_assert(O_COL + MT * VN <= 512, "TMEM");
+    static_assert(COLS <= 512, "TMEM");
     static_assert(Q_TILE % 1024 == 0 && C_CHUNK % 1024 == 0 && K_BYTES % 1024 == 0, "swizzle atoms stay aligned");
 };
 
@@ -101,7 +105,10 @@ struct Misc {
     uint64_t p_full[2];   // its probabilities are in TMEM
     uint64_t o_done[2];   // its output MMA has finished (MT = 2: the last item's only, as s_full of
                           // item w + 2 says so of the others: its MMAs come after PV(w))
-    uint64_t x_full, x_empty;  // a pair: the other CTA's scores of an item are here; it has read mine
+    // a pair, per item: the other CTA's scores are here; they are read here; they
+    // are read there; this CTA's are read out of TMEM for sending
+    uint64_t x_full[2], x_read[2], x_empty[2], x_taken[2];
+    uint64_t q_tmem;  // QT: the latent queries are in TMEM
     uint64_t q_full;
     uint64_t drain;
     uint32_t tmem_base;
@@ -208,8 +215,13 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             mbar_init(&misc.p_full[i], 4);
             mbar_init(&misc.o_done[i], 1);
         }
-        mbar_init(&misc.x_full, 1);
-        mbar_init(&misc.x_empty, 4);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&misc.x_full[i], 1);
+            mbar_init(&misc.x_read[i], 4);
+            mbar_init(&misc.x_empty[i], 1);
+            mbar_init(&misc.x_taken[i], 4);
+        }
+        mbar_init(&misc.q_tmem, 4);
         mbar_init(&misc.q_full, 1);
         mbar_init(&misc.drain, 1);
         misc.abort_flag = 0;
@@ -273,13 +285,13 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             const int box = min(P, C::KT);
             bool ok = true;
             if (lane == 0) {
-                mbar_arrive_expect_tx(&misc.q_full, C::MT * (C::NCH * C::Q_CHUNK + (has_rope ? C::QR_BYTES : 0)));
+                mbar_arrive_expect_tx(&misc.q_full, C::MT * (C::Q_LAT + (has_rope ? C::QR_BYTES : 0)));
                 for (int m = 0; m < C::MT; ++m) {
                     uint8_t* dst = sm + C::OFF_Q + m * C::Q_TILE;
                     const int y = (int)out0 + m * 128;
-                    for (int c = 0; c < C::NCH; ++c)
+                    for (int c = 0; !C::QT && c < C::NCH; ++c)
                         tma_load_2d(dst + c * C::Q_CHUNK, &maps.q, col0 + c * 64, y, &misc.q_full);
-                    if (has_rope) tma_load_2d(dst + C::NCH * C::Q_CHUNK, &maps.qr, rope0, y, &misc.q_full);
+                    if (has_rope) tma_load_2d(dst + C::Q_LAT, &maps.qr, rope0, y, &misc.q_full);
                 }
             }
             int win = 0, page_of_lane = 0;  // 32 block-table entries from `win` on
@@ -334,7 +346,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             constexpr uint32_t ID_O = idesc_bf16_f32(128, C::VN, false, true);
             const uint32_t base = smem_u32(sm);
             const uint64_t dQ = smem_desc(base + C::OFF_Q, 16, 1024, kLayoutSw128);
-            const uint64_t dQr = rope_desc<C::RL>(base + C::OFF_Q + C::NCH * C::Q_CHUNK);
+            const uint64_t dQr = rope_desc<C::RL>(base + C::OFF_Q + C::Q_LAT);
             const uint64_t dC = smem_desc(base + C::OFF_C, 16, 1024, kLayoutSw128);           // K-major
             const uint64_t dV = smem_desc(base + C::OFF_C, C::C_CHUNK, 1024, kLayoutSw128);  // MN-major
             const uint64_t dK = rope_desc<C::RL>(base + C::OFF_K);
@@ -356,9 +368,11 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                 for (int k = 0; k < C::RL / 16; ++k)
                     if (has_rope) mma_bf16(d, qr + 2 * k, k0 + 2 * k, ID_S, k ? 1u : 0u);
 #pragma unroll
-                for (int k = 0; k < C::DL / 16; ++k)
-                    mma_bf16(d, q + ((k / 4 * C::Q_CHUNK) >> 4) + k % 4 * 2, c + ((k / 4 * C::C_CHUNK) >> 4) + k % 4 * 2, ID_S,
-                             k || has_rope ? 1u : 0u);
+                for (int k = 0; k < C::DL / 16; ++k) {
+                    const uint64_t ck = c + ((k / 4 * C::C_CHUNK) >> 4) + k % 4 * 2;
+                    if constexpr (C::QT) mma_bf16_ts(d, tmem + C::Q_COL + 8 * k, ck, ID_S, k || has_rope ? 1u : 0u);
+                    else mma_bf16(d, q + ((k / 4 * C::Q_CHUNK) >> 4) + k % 4 * 2, ck, ID_S, k || has_rope ? 1u : 0u);
+                }
                 mma_commit(&misc.s_full[slot]);
                 if (m == C::MT - 1) mma_commit(&misc.k_empty[k_new.at]);
             };
@@ -371,6 +385,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                 if (m == C::MT - 1) mma_commit(&misc.c_empty[c_old.at]);
             };
             bool ok = mbar_wait_warp(&misc.q_full, 0);
+            if constexpr (C::QT) ok = ok && mbar_wait_warp(&misc.q_tmem, 0);
             // the first scores: of both row tiles, or of the first two token tiles
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -409,6 +424,53 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             __syncwarp();
             mbar_wait(&misc.drain, 0, 200000000ull);
             __syncwarp();
+        } else if (C::PAIR && warp == 3) {
+            // ------------------------------------------------------------ pair: room for the other CTA's scores
+            // (a warp of its own: the arrival over there releases what its thread
+            // wrote, and a thread that has just sent scores waits 1000 cycles for that)
+            bool ok = true;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&misc.x_full[0], C::X_BYTES);
+                mbar_arrive_expect_tx(&misc.x_full[1], C::X_BYTES);
+            }
+            for (int w = 0; w + 2 < nitems; ++w) {
+                ok = mbar_wait_warp(&misc.x_read[w & 1], (w >> 1) & 1);
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&misc.x_full[w & 1], C::X_BYTES);
+                    mbar_arrive_cluster(map_shared_rank(smem_u32(&misc.x_empty[w & 1]), rank ^ 1));
+                }
+                __syncwarp();
+            }
+            if (!ok && lane == 0) *abort_flag = 1;
+        } else if (C::PAIR && warp >= 8) {
+            // ------------------------------------------------------------ pair: this CTA's share of the scores
+            // each thread sends its row to the same thread of the other CTA, as
+            // [four tokens][row] of 16 bytes, while the softmax is an item behind
+            const int r = (warp & 3) * 32 + lane;
+            const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+            const uint32_t there = map_shared_rank(smem_u32(sm + C::OFF_X) + r * 16, rank ^ 1);
+            const uint32_t full = map_shared_rank(smem_u32(&misc.x_full[0]), rank ^ 1);
+            bool ok = true;
+            for (int w = 0; w < nitems && ok; ++w) {
+                ok = mbar_wait_warp(&misc.s_full[w & 1], (w >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t x[C::KT];
+#pragma unroll
+                for (int c = 0; c < C::KT / 32; ++c) tmem_ld32(lanes + (w & 1) * C::S_COLS + 32 * c, x + 32 * c);
+                tmem_wait_ld();
+                reg_tie<C::KT>(x);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&misc.x_taken[w & 1]);
+                if (w >= 2) ok = mbar_wait_warp(&misc.x_empty[w & 1], ((w >> 1) - 1) & 1);
+                if (!ok) break;
+#pragma unroll
+                for (int c = 0; c < C::KT / 4; ++c)
+                    st_async_v4(there + (w & 1) * C::X_BYTES + c * 2048, full + (w & 1) * 8, x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+            }
+            if (!ok && lane == 0) *abort_flag = 1;
         } else if (warp >= 4) {
             // ------------------------------------------------------------ softmax
             if constexpr (C::MT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
@@ -424,6 +486,25 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             // masked score, infinite, stays so)
             const float sc = a.scale_log2 == 0.f ? 1e-30f : a.scale_log2;
             const int L = past + rows / H;
+            if constexpr (C::QT) {
+                // this row's latent queries into TMEM (rows past the last: zeros)
+                const bool real = (long long)out0 + r < (long long)a.tokens * H;
+                const uint4* src = reinterpret_cast<const uint4*>(a.q_lat + (out0 + r) * W + col0);
+#pragma unroll
+                for (int c = 0; c < C::NCH; ++c) {
+                    uint32_t q[32];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        const uint4 v = real ? __ldg(src + 8 * c + u) : make_uint4(0u, 0u, 0u, 0u);
+                        q[4 * u] = v.x, q[4 * u + 1] = v.y, q[4 * u + 2] = v.z, q[4 * u + 3] = v.w;
+                    }
+                    tmem_st32(lanes + C::Q_COL + 32 * c, q);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&misc.q_tmem);
+            }
             {
                 // every page of the sequence has to lie in the pool
                 bool bad = false;
@@ -448,19 +529,10 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                 tmem_wait_ld();
                 reg_tie<C::KT>(x);
                 if constexpr (C::PAIR) {
-                    // the scores of the other CTA's columns: each thread sends its row's share
-                    // to the same thread there, [four tokens][row] of 16 bytes, and adds what
-                    // it gets (a sum of two, so both CTAs have the same bits)
-                    float4* here = reinterpret_cast<float4*>(sm + C::OFF_X) + r;
-                    const uint32_t there = map_shared_rank(smem_u32(here), rank ^ 1);
-                    const uint32_t full = map_shared_rank(smem_u32(&misc.x_full), rank ^ 1);
-                    if (r == 0) mbar_arrive_expect_tx(&misc.x_full, C::X_BYTES);
-                    if (w > 0) ok = mbar_wait_warp(&misc.x_empty, (w - 1) & 1);
-                    if (!ok) break;
-#pragma unroll
-                    for (int c = 0; c < C::KT / 4; ++c)
-                        st_async_v4(there + c * 2048, full, x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
-                    ok = mbar_wait_warp(&misc.x_full, w & 1);
+                    // plus the scores of the other CTA's columns (a sum of two, so both
+                    // CTAs have the same bits)
+                    const float4* here = reinterpret_cast<const float4*>(sm + C::OFF_X + slot * C::X_BYTES) + r;
+                    ok = mbar_wait_warp(&misc.x_full[slot], (w >> 1) & 1);
                     if (!ok) break;
 #pragma unroll
                     for (int c = 0; c < C::KT / 4; ++c) {
@@ -471,7 +543,11 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                         x[4 * c + 3] = __float_as_uint(__uint_as_float(x[4 * c + 3]) + v.w);
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(map_shared_rank(smem_u32(&misc.x_empty), rank ^ 1));
+                    if (lane == 0) mbar_arrive(&misc.x_read[slot]);
+                    // (P will lie over the scores: they have been taken for sending)
+                    ok = mbar_wait_warp(&misc.x_taken[slot], (w >> 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
                 }
                 // tokens j > limit of the tile are masked (a whole warp's rows at once see it all otherwise)
                 const int limit = pos - tok0;

@@ -20,8 +20,10 @@
 //  - a probability into three e5m2 parts: each takes the leading 3 bits of
 //    what is left (the upper byte of a half is an e5m2 value), the last one
 //    rounded: 9 significant bits, 2^-9 of it.  e5m2 because its exponent is
-//    fp16's: with the maximum at 2^7 .. 2^15 a weight down to 2^-24 of the
-//    largest is not lost, and long flat tails are made of those.
+//    fp16's; the second and third part are scaled up by 2^2 and 2^5 (their
+//    columns are summed apart), so that nothing above 2^-22 is lost: with the
+//    largest weight at 2^2 .. 2^15 that is 2^-24 of it, and long flat tails are
+//    made of such weights.
 // The value scales go into the probabilities:
 //   z_t = log2(e) scale s_t + log2 sigma_t,  w_t = 2^(z_t - M) = p_t sigma_t,
 //   o = sum w_t e_t / l,  l = sum w_t / sigma_t,
@@ -57,11 +59,11 @@ namespace {
 constexpr int kHP = 16;       // heads per tile
 constexpr int kSN = 2 * kHP;  // score columns of a branch: hi and lo query parts
 constexpr int kPN = 3 * kHP;  // output columns of a block: three probability parts
-constexpr int kMaxStages = 10;
+constexpr int kMaxStages = 9;
 constexpr int kMaxSteps = 5;
-// the reference M sits 2^kBase below the largest weight when it is set, and a
-// weight may pass that by 2^kRescaleLog2: at most 2^15, e5m2 holds 1.75 2^15
-constexpr float kBase = 7.0f;
+// the reference M sits 2^kBase below the largest weight when it is set, and is
+// raised when a weight passes 2^kTop (e5m2 holds 1.75 2^15)
+constexpr float kBase = 2.0f, kTop = 15.0f;
 constexpr int kGroups = 4;                      // softmax groups of four warps
 constexpr int kSoft = kGroups * 128;            // softmax threads
 constexpr int kFp8Threads = 128 + kSoft;        // and the copy, MMA and helper warps
@@ -134,10 +136,11 @@ struct Misc {
     int plan[4];
     int last_seg[4];
     int merge_flag;
-    int raise[kGroups][2];    // tile t (t & 1): some warp of the group needs a higher reference
+    float q_max[4 * kGroups];     // largest query magnitude seen by each softmax warp
+    uint8_t raise[kGroups][2];    // tile t (t & 1): some warp of the group needs a higher reference
     float red[kGroups][4][kHP];       // [group][quadrant][head]: maxima of a raise, at the end sums
     alignas(16) float m_run[kGroups][kHP];  // references M; read as float4
-    float factor[kGroups][kHP];       // a range's start: largest query magnitude of each warp; a raise: what O and l shrink by; its end: 1 / l
+    float factor[kGroups][kHP];       // a raise: what O and l shrink by; at the end 1 / l
 };
 static_assert(offsetof(Misc, m_run) % 16 == 0, "float4 access");
 
@@ -169,6 +172,11 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
 __device__ __forceinline__ uint32_t half_rest(uint32_t h) {
     uint32_t r;
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(h & 0xff00ff00u));
+    return r;
+}
+__device__ __forceinline__ uint32_t half_times(uint32_t h, uint32_t k2) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(k2));
     return r;
 }
 // The upper bytes of four halves.
@@ -449,6 +457,28 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
             __syncwarp();
             mbar_wait(&misc.drain[1], 0, 200000000ull);
             __syncwarp();
+        } else if (warp == 3) {
+            // ------------------------------------------------------------ the merge's sequence
+            // this CTA's last range, and whether the owner of its last tile merges it
+            // (as in decode_tc.cu: no later sequence starts in that window)
+            int last_n = -1, last_cum = 0, last_tiles = 0;
+            while (next_segment(a, n, cum, A0, A1, L, tiles, tb, te, next_len)) {
+                last_n = n, last_cum = cum, last_tiles = tiles;
+                finish_segment(n, cum, tiles);
+            }
+            if (lane == 0 && last_n >= 0) {
+                int c1_member = 1;
+                const int c1 = (last_cum + (last_tiles - 1) * kTileCost) / chunk;
+                for (int m = last_n + 1; m < a.batch; ++m) {
+                    if (seq_tiles(__ldg(a.seqlens + m), P, a.max_pages) == 0) continue;
+                    c1_member = (last_cum + last_tiles * kTileCost + kSeqCost) / chunk != c1;
+                    break;
+                }
+                misc.last_seg[0] = last_n;
+                misc.last_seg[1] = last_cum;
+                misc.last_seg[2] = last_tiles;
+                misc.last_seg[3] = c1_member;
+            }
         } else if (warp >= 4) {
             // ------------------------------------------------------------ queries, softmax, epilogue
             constexpr int HG = C::HG;
@@ -465,117 +495,127 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
             bool dead = false;
             int pend_a = -1, pend_b = -1;
 
-            // (all groups walk every range, so that they meet at the barrier
-            // below even when one has given up; then all stop)
-            for (; next_segment(a, n, cum, A0, A1, L, tiles, tb, te, next_len); finish_segment(n, cum, tiles)) {
-                // ---------------------------------------------------- queries
-                // (the range before has no score MMA left: its last step's
-                // probabilities are written).  16 head rows; heads past the last
-                // are zero.
-                float alpha_q;  // a score of the MMA times this is in log2 units (without sigma)
-                {
-                    constexpr int UPR = C::W / 8;               // 8-value units per head row
-                    constexpr int UNITS = kHP * UPR;
-                    constexpr int U = (UNITS + kSoft - 1) / kSoft;
-                    const int sid = threadIdx.x - 128;
-                    const __nv_bfloat16* q = a.q_lat + ((size_t)n * H + grp.h0) * C::W;
-                    uint4 v[U];
-                    uint32_t mx = 0;
+            // A range: its tiles, and what this thread has in hand when they begin:
+            // its token's page one tile ahead, its scale, and the query unit.
+            struct Range {
+                int n, cum, L, tiles, tb, te;
+                int page_next;
+                float sig, alpha_q;
+                bool bad;
+            };
+            auto page_of = [&](const Range& r, int j) {
+                return j < r.te && j * kT + row < r.L ? __ldg(a.block_table + (size_t)r.n * a.max_pages + ((j * kT + row) >> log_p)) : 0;
+            };
+            auto scale_of = [&](Range& r, int page, int j) {
+                const bool real = page >= 0 && page < a.num_pages;
+                r.bad |= !real;
+                return __ldg(latent_scale + (((size_t)(real ? page : 0) << log_p) + ((j * kT + row) & (P - 1))) / kFp8Block * NB + br);
+            };
+            // The next range, its queries split and written to shared memory (all
+            // groups; their score MMAs of the range before are over).  False: none is
+            // left, or a group has given up.
+            auto begin_range = [&](Range& r) {
+                if (!next_segment(a, n, cum, A0, A1, L, tiles, tb, te, next_len)) return false;
+                r.n = n, r.cum = cum, r.L = L, r.tiles = tiles, r.tb = tb, r.te = te, r.bad = false;
+                finish_segment(n, cum, tiles);
+                const int page = page_of(r, r.tb);
+                r.page_next = page_of(r, r.tb + 1);
+                // 16 head rows; heads past the last are zero
+                constexpr int UPR = C::W / 8;               // 8-value units per head row
+                constexpr int UNITS = kHP * UPR;
+                constexpr int U = (UNITS + kSoft - 1) / kSoft;
+                const int sid = threadIdx.x - 128;
+                const __nv_bfloat16* q = a.q_lat + ((size_t)r.n * H + grp.h0) * C::W;
+                uint4 v[U];
 #pragma unroll
-                    for (int i = 0; i < U; ++i) {
-                        const int u = sid + kSoft * i;
-                        v[i] = u < UNITS && u / UPR < grp.hn ? __ldg(reinterpret_cast<const uint4*>(q + (size_t)(u / UPR) * C::W) + u % UPR)
-                                                             : make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    constexpr int RU = DR / 8;                  // 16-byte units of a RoPE row
-                    uint4 rv = make_uint4(0u, 0u, 0u, 0u);
-                    if (sid < kHP * RU && sid / RU < grp.hn)
-                        rv = __ldg(reinterpret_cast<const uint4*>(a.q_rope + ((size_t)n * H + grp.h0 + sid / RU) * DR) + sid % RU);
-#pragma unroll
-                    for (int i = 0; i < U; ++i) {
-                        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t lo = w[k] & 0x7fffu, hi = (w[k] >> 16) & 0x7fffu;
-                            mx = max(mx, lo < 0x7f80u ? lo : 0u);
-                            mx = max(mx, hi < 0x7f80u ? hi : 0u);
-                        }
-                    }
-                    mx = __reduce_max_sync(0xffffffffu, mx);
-                    if (lane == 0) misc.factor[sg][quad] = __uint_as_float(mx << 16);
-                    if (named_bar_or<5, kSoft>(dead)) {
-                        dead = true;
-                        break;
-                    }
-                    // (factor is written again at the first tile, whose scores wait for q_full)
-                    float top = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 4 * kGroups; ++i) top = fmaxf(top, misc.factor[i / 4][i % 4]);
-                    // the smallest power of two tau with top <= 448 tau (2^-100 at least: both it
-                    // and its reciprocal are normal numbers)
-                    const uint32_t tb32 = __float_as_uint(top);
-                    const int e = max((int)(tb32 >> 23) - 135 + ((tb32 & 0x7fffffu) > 0x600000u), -100);
-                    const float inv_tau = __uint_as_float((uint32_t)(127 - e) << 23);
-                    alpha_q = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
-                    if (sid < kHP * RU) {
-                        const int h = sid / RU, u = sid % RU;
-                        *reinterpret_cast<uint4*>(sm + C::OFF_QR + (DR == 64 ? h * 128 + ((u ^ (h & 7)) << 4) : h * 64 + ((u ^ ((h >> 1) & 3)) << 4))) = rv;
-                    }
-#pragma unroll
-                    for (int i = 0; i < U; ++i) {
-                        const int u = sid + kSoft * i, h = u / UPR, col = u % UPR * 8;
-                        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            float x = __uint_as_float(w[k] << 16) * inv_tau, y = __uint_as_float(w[k] & 0xffff0000u) * inv_tau;
-                            x = fmaf(x, 0.f, x);  // infinities become NaN: the head's scores are NaN as in full precision
-                            y = fmaf(y, 0.f, y);
-                            hi[k] = e4m3x2(x, y);
-                            const float2 f = from_e4m3x2(hi[k]);
-                            lo[k] = e4m3x2(x - f.x, y - f.y);
-                        }
-                        if (u < UNITS) {
-                            uint8_t* dst = sm + C::OFF_Q + col / 128 * C::Q_CHUNK_BYTES + h * 128 +
-                                           (((col % 128 / 16) ^ (h & 7)) << 4) + col % 16;
-                            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-                            *reinterpret_cast<uint2*>(dst + kHP * 128) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&misc.q_full);
+                for (int i = 0; i < U; ++i) {
+                    const int u = sid + kSoft * i;
+                    v[i] = u < UNITS && u / UPR < grp.hn ? __ldg(reinterpret_cast<const uint4*>(q + (size_t)(u / UPR) * C::W) + u % UPR)
+                                                         : make_uint4(0u, 0u, 0u, 0u);
                 }
-                bool bad = false;
-                const int32_t* bt = a.block_table + (size_t)n * a.max_pages;
-                int c1_member = 1;  // as in decode_tc.cu: whether the owner of the last tile merges
-                if (threadIdx.x == 128) {
-                    const int c1 = (cum + (tiles - 1) * kTileCost) / chunk;
-                    for (int m = n + 1; m < a.batch; ++m) {
-                        if (seq_tiles(__ldg(a.seqlens + m), a.page_size, a.max_pages) == 0) continue;
-                        c1_member = (cum + tiles * kTileCost + kSeqCost) / chunk != c1;
-                        break;
+                constexpr int RU = DR / 8;                  // 16-byte units of a RoPE row
+                uint4 rv = make_uint4(0u, 0u, 0u, 0u);
+                if (sid < kHP * RU && sid / RU < grp.hn)
+                    rv = __ldg(reinterpret_cast<const uint4*>(a.q_rope + ((size_t)r.n * H + grp.h0 + sid / RU) * DR) + sid % RU);
+                uint32_t mx = 0;
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t lo = w[k] & 0x7fffu, hi = (w[k] >> 16) & 0x7fffu;
+                        mx = max(mx, lo < 0x7f80u ? lo : 0u);
+                        mx = max(mx, hi < 0x7f80u ? hi : 0u);
                     }
                 }
+                mx = __reduce_max_sync(0xffffffffu, mx);
+                if (lane == 0) misc.q_max[warp - 4] = __uint_as_float(mx << 16);
+                // (every group comes here for every range, also one that has given up:
+                // then all stop)
+                if (named_bar_or<5, kSoft>(dead)) {
+                    dead = true;
+                    return false;
+                }
+                r.sig = scale_of(r, page, r.tb);
+                // (q_max is written again after this range's tiles, whose scores wait for
+                // every warp's q_full)
+                float top = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4 * kGroups; ++i) top = fmaxf(top, misc.q_max[i]);
+                // the smallest power of two tau with top <= 448 tau (2^-100 at least: both it
+                // and its reciprocal are normal numbers); a score of the MMA times alpha_q is
+                // in log2 units (without sigma)
+                const uint32_t bits = __float_as_uint(top);
+                const int e = max((int)(bits >> 23) - 135 + ((bits & 0x7fffffu) > 0x600000u), -100);
+                const float inv_tau = __uint_as_float((uint32_t)(127 - e) << 23);
+                r.alpha_q = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+                if (sid < kHP * RU) {
+                    const int h = sid / RU, u = sid % RU;
+                    *reinterpret_cast<uint4*>(sm + C::OFF_QR + (DR == 64 ? h * 128 + ((u ^ (h & 7)) << 4) : h * 64 + ((u ^ ((h >> 1) & 3)) << 4))) = rv;
+                }
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    const int u = sid + kSoft * i, h = u / UPR, col = u % UPR * 8;
+                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float x = __uint_as_float(w[k] << 16) * inv_tau, y = __uint_as_float(w[k] & 0xffff0000u) * inv_tau;
+                        x = fmaf(x, 0.f, x);  // infinities become NaN: the head's scores are NaN as in full precision
+                        y = fmaf(y, 0.f, y);
+                        hi[k] = e4m3x2(x, y);
+                        const float2 f = from_e4m3x2(hi[k]);
+                        lo[k] = e4m3x2(x - f.x, y - f.y);
+                    }
+                    if (u < UNITS) {
+                        uint8_t* dst = sm + C::OFF_Q + col / 128 * C::Q_CHUNK_BYTES + h * 128 +
+                                       (((col % 128 / 16) ^ (h & 7)) << 4) + col % 16;
+                        *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+                        *reinterpret_cast<uint2*>(dst + kHP * 128) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&misc.q_full);
+                return true;
+            };
 
-                // this thread's token: its page two tiles ahead, its scale one
-                auto page_of = [&](int j) { return j < te && j * kT + row < L ? __ldg(bt + ((j * kT + row) >> log_p)) : 0; };
-                auto scale_of = [&](int page, int j) {
-                    const bool real = page >= 0 && page < a.num_pages;
-                    bad |= !real;
-                    return __ldg(latent_scale + (((size_t)(real ? page : 0) << log_p) + ((j * kT + row) & (P - 1))) / kFp8Block * NB + br);
-                };
-                int page_next = page_of(tb + 1);
-                float sig = scale_of(page_of(tb), tb), sig_next = 0.f;
+            Range rg;
+            bool more = begin_range(rg);
+            while (more) {  // (a group that has given up goes on to the barrier in begin_range)
+                const int tb = rg.tb, te = rg.te;
+                const float alpha_q = rg.alpha_q;
+                int page_next = rg.page_next;
+                float sig = rg.sig, sig_next = 0.f;
                 float l[HG];  // this thread's share of sum w / sigma
 #pragma unroll
                 for (int i = 0; i < HG; ++i) l[i] = 0.f;
 
                 for (int j = tb; j < te && !dead; ++j, ++tcnt) {
                     const uint32_t gs = tcnt * C::NSTEP + st, slot = gs % C::NSP, parity = (gs / C::NSP) & 1;
-                    const bool masked = j * kT + row >= L;
-                    const int page_after = page_of(j + 2);
-                    if (j + 1 < te) sig_next = scale_of(page_next, j + 1);
+                    const bool masked = j * kT + row >= rg.L;
+                    const int page_after = page_of(rg, j + 2);
+                    if (j + 1 < te) sig_next = scale_of(rg, page_next, j + 1);
                     page_next = page_after;
                     const float ls = fast_log2(sig), k = sig * alpha_q;
                     const float rs = masked ? 0.f : __frcp_rn(sig);
@@ -626,8 +666,9 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                             if (part > 0) {
 #pragma unroll
                                 for (int i = 0; i < HG / 2; ++i) {
-                                    h[i] = half_rest(h[i]);
-                                    if (part == 2) h[i] += 0x00800080u;  // the last part is rounded, not cut
+                                    // (exact: times 4, times 8; the last part is rounded, not cut)
+                                    h[i] = half_times(half_rest(h[i]), part == 1 ? 0x44004400u : 0x48004800u);
+                                    if (part == 2) h[i] += 0x00800080u;
                                 }
                             }
                             if constexpr (HG == 16)
@@ -650,9 +691,9 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                         float top = z[0];
 #pragma unroll
                         for (int i = 1; i < HG; ++i) top = fmaxf(top, z[i]);
-                        const bool need = __any_sync(0xffffffffu, top > kBase + kRescaleLog2 || !ok);
+                        const bool need = __any_sync(0xffffffffu, top > kTop || !ok);
                         if (lane == 0) {
-                            if (need) *reinterpret_cast<volatile int*>(&misc.raise[sg][tcnt & 1]) = 1;
+                            if (need) *reinterpret_cast<volatile uint8_t*>(&misc.raise[sg][tcnt & 1]) = 1;
                             mbar_arrive(&misc.vote[sg]);
                         }
                         write_weights();
@@ -661,7 +702,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                     }
                     // (every warp votes: what it waits for before is bounded well below this)
                     const bool ok1 = mbar_wait(&misc.vote[sg], tcnt & 1, 8000000000ull);
-                    raise |= *reinterpret_cast<volatile int*>(&misc.raise[sg][tcnt & 1]) != 0;
+                    raise |= *reinterpret_cast<volatile uint8_t*>(&misc.raise[sg][tcnt & 1]) != 0;
                     if (!ok1 || raise) {
                         // all four warps: exact column maxima, new references, O and l at
                         // them, the weights again
@@ -735,9 +776,13 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                     if (lane == 0) mbar_arrive(&misc.p_full[slot]);
                     sig = sig_next;
                 }
-                if (dead) continue;
+                // the next range's queries now: its scores are made during the epilogue
+                const Range rd = rg;
+                more = begin_range(rg);
+                if (dead) break;
 
                 // ---------------------------------------------------- epilogue
+                const int n = rd.n, cum = rd.cum, tiles = rd.tiles;
                 {
                     float f[HG];
 #pragma unroll
@@ -746,7 +791,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                     constexpr int SPAN = 32 / HG;
                     if ((lane & (SPAN - 1)) == 0) misc.red[sg][quad][lane / SPAN] = f[0];
                 }
-                bad = named_bar_or_id<128>(gbar, bad);  // also publishes red
+                const bool bad = named_bar_or_id<128>(gbar, rd.bad);  // also publishes red
                 const bool single = cum >= A0 && cum + (tiles - 1) * kTileCost < A1;
                 const size_t slot = (size_t)grp.slot0 + grp.ci + n;
                 if (row < HG) {
@@ -783,7 +828,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                         tmem_wait_ld();
                         if (!mine) continue;
 #pragma unroll
-                        for (int i = 0; i < N; ++i) o[i] = bad ? 0.f : (o[i] + (o1[i] + o2[i])) * misc.factor[sg][i0 + i];
+                        for (int i = 0; i < N; ++i) o[i] = bad ? 0.f : fmaf(o2[i], 1.f / 32, fmaf(o1[i], 0.25f, o[i])) * misc.factor[sg][i0 + i];
                         if (single) {
                             const int h0 = hoff + i0;
                             __nv_bfloat16* dst = a.out + (((size_t)n * H + grp.h0 + h0) * NB + br) * DC + col;
@@ -802,14 +847,8 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                 if (bad && row == 0) record_error(a.err, MLRA_ERR_DEVICE_BAD_INDEX);
                 tc_fence_before();
                 named_bar_sync_id<128>(gbar);  // factor and red are reused by the next range
-                if (threadIdx.x == 128) {
-                    if (!single) {
-                        if (pend_a < 0) pend_a = n; else pend_b = n;
-                    }
-                    misc.last_seg[0] = n;
-                    misc.last_seg[1] = cum;
-                    misc.last_seg[2] = tiles;
-                    misc.last_seg[3] = c1_member;
+                if (threadIdx.x == 128 && !single) {
+                    if (pend_a < 0) pend_a = n; else pend_b = n;
                 }
             }
             if (dead && row == 0) {

@@ -85,7 +85,8 @@ __device__ __forceinline__ void record_error(int* err, int code) {
 // L_n is invalid.  Work is counted in cost units: a tile costs kTileCost, and
 // every sequence adds kSeqCost after its last tile for the per-segment work
 // (query load, first-tile setup, epilogue) that a CTA pays each time its range
-// enters a new sequence.  Sequence n occupies the cost interval
+// enters a new sequence (the kernels below take that charge as a template
+// parameter: it is what a range change costs the kernel at hand).  Sequence n occupies the cost interval
 // [cum_n, cum_n + cost_n), cost_n = kTileCost * tiles_n + kSeqCost, and its
 // tile t starts at cum_n + kTileCost * t.  With
 //   chunk = kTileCost * max(ceil(total_cost / (num_ctas * kTileCost)), 1)
@@ -111,9 +112,10 @@ __device__ __forceinline__ int seq_tiles(int L, int page_size, int max_pages) {
     return seqlen_valid(L, page_size, max_pages) ? (L + kTileTokens - 1) / kTileTokens : 0;
 }
 
+template <int SEQ = kSeqCost>
 __device__ __forceinline__ int seq_cost(int L, int page_size, int max_pages) {
     const int t = seq_tiles(L, page_size, max_pages);
-    return t > 0 ? t * kTileCost + kSeqCost : 0;
+    return t > 0 ? t * kTileCost + SEQ : 0;
 }
 
 __host__ __device__ __forceinline__ int plan_chunk(int total_cost, int num_ctas) {
@@ -131,10 +133,11 @@ __device__ __forceinline__ int first_tile_at(int cum, int tiles, int A) {
 }
 
 // Whole warp: sum of the costs of sequences [0, n).
+template <int SEQ = kSeqCost>
 __device__ inline int warp_cost_prefix(const int32_t* seqlens, int n, int P, int max_pages) {
     const int lane = threadIdx.x & 31;
     int sum = 0;
-    for (int m = lane; m < n; m += 32) sum += seq_cost(__ldg(seqlens + m), P, max_pages);
+    for (int m = lane; m < n; m += 32) sum += seq_cost<SEQ>(__ldg(seqlens + m), P, max_pages);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     return sum;
@@ -142,13 +145,14 @@ __device__ inline int warp_cost_prefix(const int32_t* seqlens, int n, int P, int
 
 // Whole warp: the first sequence with a tile starting at or after position A,
 // and its cost start (batch and the total cost if there is none).
+template <int SEQ = kSeqCost>
 __device__ inline void warp_find_seq(const int32_t* seqlens, int batch, int P, int max_pages,
                                      int A, int* seq_out, int* cum_out) {
     const int lane = threadIdx.x & 31;
     int base_cum = 0;
     for (int base = 0; base < batch; base += 32) {
         const int n = base + lane;
-        const int c = n < batch ? seq_cost(__ldg(seqlens + n), P, max_pages) : 0;
+        const int c = n < batch ? seq_cost<SEQ>(__ldg(seqlens + n), P, max_pages) : 0;
         int incl = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -156,9 +160,9 @@ __device__ inline void warp_find_seq(const int32_t* seqlens, int batch, int P, i
             if (lane >= o) incl += v;
         }
         const int excl = incl - c;
-        // last tile start = cum + cost - kSeqCost - kTileCost
+        // last tile start = cum + cost - SEQ - kTileCost
         const unsigned hit = __ballot_sync(0xffffffffu,
-                                           c > 0 && base_cum + incl - kSeqCost - kTileCost >= A);
+                                           c > 0 && base_cum + incl - SEQ - kTileCost >= A);
         if (hit) {
             const int src = __ffs(hit) - 1;
             *seq_out = base + src;

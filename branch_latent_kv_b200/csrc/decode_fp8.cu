@@ -74,6 +74,12 @@ struct Cfg {
     static constexpr int NCH = W / 128;                          // 128-byte chunks of a token row
     static constexpr int BPC = DC >= 128 ? 1 : 128 / DC;         // branches per chunk
     static constexpr int SBR = BPC;                              // branches per step (a chunk is not divided)
+    // a range change in cost units of the split plan (a tile is 8): new queries,
+    // the first tile's references and an epilogue take about two tiles' time.
+    // 16 x 8192 tokens of four branches: 34.3 us at 4, 33.8 at 12, 32.7 at 20; the
+    // ragged batch 98.8, 98.4, 93.0; one 512-wide branch (a quarter of the
+    // softmax) 72.2 at 4, 71.1 at 12, 73.3 at 20.
+    static constexpr int RANGE_COST = NB == 1 ? 12 : 20;
     static constexpr int HG = kHP * NB / kGroups;                // heads of a softmax group: 16, 8 or 4
     static constexpr int GPB = kGroups / NB;                     // groups per branch
     static constexpr int GPS = GPB * SBR;                        // groups per step
@@ -222,12 +228,12 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
     int n_first, cum_first;
     if (warp == 0) {
         wait_prerequisite_grid();
-        const int total = warp_cost_prefix(a.seqlens, a.batch, P, a.max_pages);
+        const int total = warp_cost_prefix<C::RANGE_COST>(a.seqlens, a.batch, P, a.max_pages);
         const int chunk = plan_chunk(total, grp.cpg);
         n_first = a.batch;
         cum_first = total;
         if (!grp.idle && (long long)grp.ci * chunk < total)
-            warp_find_seq(a.seqlens, a.batch, P, a.max_pages, grp.ci * chunk, &n_first, &cum_first);
+            warp_find_seq<C::RANGE_COST>(a.seqlens, a.batch, P, a.max_pages, grp.ci * chunk, &n_first, &cum_first);
         if (lane == 0) {
             misc.plan[1] = chunk;
             misc.plan[2] = n_first;
@@ -269,7 +275,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
             uint32_t cc = 0, tc = 0;  // chunks and tiles issued
             const uint64_t policy = grp.cpg == a.num_ctas ? l2_policy_evict_first() : l2_policy_evict_normal();
             bool ok = true;
-            while (ok && next_segment(a, n, cum, A0, A1, L, tiles, tb, te, next_len)) {
+            while (ok && next_segment<C::RANGE_COST>(a, n, cum, A0, A1, L, tiles, tb, te, next_len)) {
                 const int32_t* bt = a.block_table + (size_t)n * a.max_pages;
                 int win_base = tb * kT / P, win_val = 0;  // 32 block-table entries, one per lane
                 if (win_base + lane < a.max_pages) win_val = __ldg(bt + win_base + lane);
@@ -315,7 +321,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                     }
                     ok = __shfl_sync(0xffffffffu, ok && !*abort_flag, 0);
                 }
-                finish_segment(n, cum, tiles);
+                finish_segment<C::RANGE_COST>(n, cum, tiles);
             }
             if (lane == 0) {
                 if (!ok) {
@@ -343,7 +349,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
             const uint64_t dR = rope_desc<DR>(base + C::OFF_ROPE);
             uint32_t gs = 0, tc = 0, sc = 0, stage = 0, phase = 0;
             bool ok = true;
-            while (ok && next_segment(a, n, cum, A0, A1, L, tiles, tb, te, next_len)) {
+            while (ok && next_segment<C::RANGE_COST>(a, n, cum, A0, A1, L, tiles, tb, te, next_len)) {
                 ok = mbar_wait_warp(&misc.q_full, sc & 1);
                 tc_fence_after();
                 for (int j = tb; j < te && ok; ++j) {
@@ -394,7 +400,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                     if (__shfl_sync(0xffffffffu, *abort_flag, 0)) ok = false;
                 }
                 ++sc;
-                finish_segment(n, cum, tiles);
+                finish_segment<C::RANGE_COST>(n, cum, tiles);
             }
             if (!ok && lane == 0) {
                 record_error(a.err, MLRA_ERR_DEVICE_TIMEOUT);
@@ -414,7 +420,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
             const uint64_t dP = smem_desc(base + C::OFF_P, 128, C::P_PART_BYTES, kLayoutNone);
             uint32_t gs = 0, stage = 0;
             bool ok = true;
-            while (ok && next_segment(a, n, cum, A0, A1, L, tiles, tb, te, next_len)) {
+            while (ok && next_segment<C::RANGE_COST>(a, n, cum, A0, A1, L, tiles, tb, te, next_len)) {
                 for (int j = tb; j < te && ok; ++j) {
 #pragma unroll 1
                     for (int st = 0; st < C::NSTEP; ++st) {
@@ -447,7 +453,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                     }
                     if (__shfl_sync(0xffffffffu, *abort_flag, 0)) ok = false;
                 }
-                finish_segment(n, cum, tiles);
+                finish_segment<C::RANGE_COST>(n, cum, tiles);
             }
             if (!ok && lane == 0) {
                 record_error(a.err, MLRA_ERR_DEVICE_TIMEOUT);
@@ -462,16 +468,16 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
             // this CTA's last range, and whether the owner of its last tile merges it
             // (as in decode_tc.cu: no later sequence starts in that window)
             int last_n = -1, last_cum = 0, last_tiles = 0;
-            while (next_segment(a, n, cum, A0, A1, L, tiles, tb, te, next_len)) {
+            while (next_segment<C::RANGE_COST>(a, n, cum, A0, A1, L, tiles, tb, te, next_len)) {
                 last_n = n, last_cum = cum, last_tiles = tiles;
-                finish_segment(n, cum, tiles);
+                finish_segment<C::RANGE_COST>(n, cum, tiles);
             }
             if (lane == 0 && last_n >= 0) {
                 int c1_member = 1;
                 const int c1 = (last_cum + (last_tiles - 1) * kTileCost) / chunk;
                 for (int m = last_n + 1; m < a.batch; ++m) {
                     if (seq_tiles(__ldg(a.seqlens + m), P, a.max_pages) == 0) continue;
-                    c1_member = (last_cum + last_tiles * kTileCost + kSeqCost) / chunk != c1;
+                    c1_member = (last_cum + last_tiles * kTileCost + C::RANGE_COST) / chunk != c1;
                     break;
                 }
                 misc.last_seg[0] = last_n;
@@ -515,9 +521,9 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
             // groups; their score MMAs of the range before are over).  False: none is
             // left, or a group has given up.
             auto begin_range = [&](Range& r) {
-                if (!next_segment(a, n, cum, A0, A1, L, tiles, tb, te, next_len)) return false;
+                if (!next_segment<C::RANGE_COST>(a, n, cum, A0, A1, L, tiles, tb, te, next_len)) return false;
                 r.n = n, r.cum = cum, r.L = L, r.tiles = tiles, r.tb = tb, r.te = te, r.bad = false;
-                finish_segment(n, cum, tiles);
+                finish_segment<C::RANGE_COST>(n, cum, tiles);
                 const int page = page_of(r, r.tb);
                 r.page_next = page_of(r, r.tb + 1);
                 // 16 head rows; heads past the last are zero

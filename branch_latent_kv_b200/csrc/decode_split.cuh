@@ -184,6 +184,7 @@ __device__ __forceinline__ int first_len(const DecodeArgs& a, int n) {
     return n < a.batch ? __ldg(a.seqlens + n) : 0;
 }
 
+template <int SEQ = kSeqCost>
 __device__ __forceinline__ bool next_segment(const DecodeArgs& a, int& n, int& cum, int A0, int A1,
                                              int& L, int& tiles, int& tb, int& te, int& next_len) {
     while (n < a.batch && cum < A1) {
@@ -194,15 +195,16 @@ __device__ __forceinline__ bool next_segment(const DecodeArgs& a, int& n, int& c
             tb = first_tile_at(cum, tiles, A0);
             te = first_tile_at(cum, tiles, A1);
             if (tb < te) return true;
-            cum += tiles * kTileCost + kSeqCost;
+            cum += tiles * kTileCost + SEQ;
         }
         ++n;
     }
     return false;
 }
 
+template <int SEQ = kSeqCost>
 __device__ __forceinline__ void finish_segment(int& n, int& cum, int tiles) {
-    cum += tiles * kTileCost + kSeqCost;
+    cum += tiles * kTileCost + SEQ;
     ++n;
 }
 

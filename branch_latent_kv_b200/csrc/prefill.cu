@@ -32,6 +32,8 @@
 // P is rounded to bf16 (the output MMA takes P and C in one type, and C is
 // bf16): half a step, 2^-8 of each probability, averaged over the row; the
 // sum is of the unrounded ones.  Scores, maxima, sums and O are fp32.
+#include <array>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
@@ -190,7 +192,8 @@ __device__ __forceinline__ uint64_t rope_desc(uint32_t addr) {
 
 template <int DC, int DR>
 __global__ void __launch_bounds__(Cfg<DC, DR>::THREADS, 1)
-prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ PrefillArgs a, const long long places) {
+prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ PrefillArgs a, const long long places,
+               const int log_splits) {
     using C = Cfg<DC, DR>;
     static_assert(sizeof(Misc) <= C::MISC, "barriers fit");
     extern __shared__ uint8_t smem_raw[];
@@ -198,13 +201,16 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
     Misc& misc = *reinterpret_cast<Misc*>(sm + C::OFF_MISC);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int H = a.heads, B = a.branches, P = a.page_size;
-    const int part = blockIdx.x % (B * C::NV), b = part / C::NV;
-    const int rank = part % C::NV;       // place in the pair (its cluster rank)
+    // a cluster: the `splits` parts of a row block's tokens, each a CTA or a pair
+    const int splits = 1 << log_splits, cluster = splits * C::NV;
+    const int crank = blockIdx.x & (cluster - 1), split = crank / C::NV, rank = crank % C::NV;
+    const uint32_t job = blockIdx.x / C::NV >> log_splits;
+    const int b = job % B;
     const int col0 = b * DC + rank * C::DL;  // this CTA's first column of a latent row
     const bool has_rope = !C::PAIR || DR == 64 || rank == 0;
     const int rope0 = C::PAIR && DR == 64 ? rank * C::RL : 0;  // its first RoPE column
     // a sequence's later row blocks see more tokens: they start first
-    const long long place = places - 1 - blockIdx.x / (B * C::NV);
+    const long long place = places - 1 - job / B;
 
     launch_dependents();
     if (threadIdx.x == 32) {
@@ -251,7 +257,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
         }
     }
     tc_fence_before();
-    if constexpr (C::PAIR) cluster_sync();  // (the other CTA's barriers are set up too)
+    if (cluster > 1) cluster_sync();  // (the other CTAs' barriers are set up too)
     else __syncthreads();
     tc_fence_after();
     const int n = misc.job[0], row0 = misc.job[1], rows = misc.job[2], past = misc.job[4];
@@ -273,7 +279,10 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
     } else if (n >= 0) {
         const int last_row = min(row0 + C::BM, rows) - 1;
         const int kv_end = past + last_row / H + 1;  // tokens that some row sees
-        const int ntiles = ceil_div(kv_end, C::KT), nitems = ntiles * C::MT;
+        // this CTA's tiles: [t0, t0 + ntiles) of all (none where there are fewer than parts)
+        const int all_tiles = ceil_div(kv_end, C::KT);
+        const int t0 = all_tiles * split >> log_splits;  // (at most 2^25 tiles, 8 parts)
+        const int ntiles = (all_tiles * (split + 1) >> log_splits) - t0, nitems = ntiles * C::MT;
         const int32_t* bt = a.block_table + (size_t)n * a.max_pages;
         volatile int* abort_flag = &misc.abort_flag;
 
@@ -294,11 +303,11 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                     if (has_rope) tma_load_2d(dst + C::Q_LAT, &maps.qr, rope0, y, &misc.q_full);
                 }
             }
-            int win = 0, page_of_lane = 0;  // 32 block-table entries from `win` on
-            if (lane < a.max_pages) page_of_lane = __ldg(bt + lane);
+            int win = t0 * C::KT / P, page_of_lane = 0;  // 32 block-table entries from `win` on
+            if (win + lane < a.max_pages) page_of_lane = __ldg(bt + win + lane);
             int done = 0;  // tiles whose copies were issued
             for (int i = 0; i < ntiles && ok; ++i) {
-                const int tok0 = i * C::KT, nbox = ceil_div(min(C::KT, kv_end - tok0), box);
+                const int tok0 = (t0 + i) * C::KT, nbox = ceil_div(min(C::KT, kv_end - tok0), box);
                 const int page0 = tok0 / P;
                 if (page0 + (nbox * box + P - 1) / P > win + 32) {
                     win = page0;
@@ -384,11 +393,11 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                 if (C::MT == 1 || last) mma_commit(&misc.o_done[slot]);
                 if (m == C::MT - 1) mma_commit(&misc.c_empty[c_old.at]);
             };
-            bool ok = mbar_wait_warp(&misc.q_full, 0);
+            bool ok = ntiles == 0 || mbar_wait_warp(&misc.q_full, 0);
             if constexpr (C::QT) ok = ok && mbar_wait_warp(&misc.q_tmem, 0);
             // the first scores: of both row tiles, or of the first two token tiles
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
+            for (int s = 0; s < 2 && ntiles > 0; ++s) {
                 if (s == 0 || C::MT == 1) ok = ok && s < ntiles && landed();
                 if (s > 0 && C::MT == 1 && s >= ntiles) ok = true;  // (one tile only)
                 else if (ok) {
@@ -438,7 +447,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                 if (!ok) break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&misc.x_full[w & 1], C::X_BYTES);
-                    mbar_arrive_cluster(map_shared_rank(smem_u32(&misc.x_empty[w & 1]), rank ^ 1));
+                    mbar_arrive_cluster(map_shared_rank(smem_u32(&misc.x_empty[w & 1]), crank ^ 1));
                 }
                 __syncwarp();
             }
@@ -449,8 +458,8 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             // [four tokens][row] of 16 bytes, while the softmax is an item behind
             const int r = (warp & 3) * 32 + lane;
             const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-            const uint32_t there = map_shared_rank(smem_u32(sm + C::OFF_X) + r * 16, rank ^ 1);
-            const uint32_t full = map_shared_rank(smem_u32(&misc.x_full[0]), rank ^ 1);
+            const uint32_t there = map_shared_rank(smem_u32(sm + C::OFF_X) + r * 16, crank ^ 1);
+            const uint32_t full = map_shared_rank(smem_u32(&misc.x_full[0]), crank ^ 1);
             bool ok = true;
             for (int w = 0; w < nitems && ok; ++w) {
                 ok = mbar_wait_warp(&misc.s_full[w & 1], (w >> 1) & 1);
@@ -518,7 +527,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             bool ok = true;
             int w = g;
             for (; w < nitems; w += C::MT) {
-                const int i = w / C::MT, slot = w & 1, tok0 = i * C::KT;
+                const int i = w / C::MT, slot = w & 1, tok0 = (t0 + i) * C::KT;
                 const uint32_t s_addr = lanes + slot * C::S_COLS;
                 ok = mbar_wait_warp(&misc.s_full[slot], (w >> 1) & 1);
                 if (!ok) break;
@@ -574,7 +583,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                     top[0] = fmaxf(max3(top[0], top[1], top[2]), top[3]) * sc;
                 }
                 if (i == 0) {
-                    mx = top[0];  // token 0 is seen by every row
+                    mx = top[0];
                 } else {
                     const bool grow = top[0] > mx + kRescale;
                     if (__any_sync(0xffffffffu, grow)) {
@@ -610,7 +619,10 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                             make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
                 }
-                const uint64_t sc2 = pack2(sc, sc), mx2 = pack2(-mx, -mx);
+                // (a row that has seen no token yet: its scores are all -infinity, and so their
+                // differences stay)
+                const float ref = mx == -INFINITY ? 0.f : mx;
+                const uint64_t sc2 = pack2(sc, sc), mx2 = pack2(-ref, -ref);
                 uint64_t sum[2] = {0, 0};
 #pragma unroll
                 for (int j = 0; j < C::KT; j += 2) {
@@ -631,7 +643,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                 unpack2(add2(sum[0], sum[1]), s0, s1);
                 l += s0 + s1;
             }
-            if (ok) {
+            if (ok && nitems > 0) {
                 const int v = w - C::MT;  // this tile's last item
                 ok = mbar_wait_warp(&misc.o_done[v & 1], C::MT == 1 ? (v >> 1) & 1 : 0);
                 tc_fence_after();
@@ -643,27 +655,89 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             named_bar_sync<1, 32 * C::SOFT_WARPS>();  // every page check is in
             const bool bad = misc.bad != 0 || !ok;
             if (misc.bad != 0 && threadIdx.x == 128 && a.status != nullptr) record_error(a.status, MLRA_ERR_DEVICE_BAD_INDEX);
-            const float inv = a.out_scale / l;
             __nv_bfloat16* dst = a.out + (out0 + g * 128 + r) * W + col0;
+            if (splits == 1) {
+                const float inv = a.out_scale / l;
 #pragma unroll 1
-            for (int c = 0; c < C::VN / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(o_addr + 32 * c, o);
-                tmem_wait_ld();
-                reg_tie<32>(o);
+                for (int c = 0; c < C::VN / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(o_addr + 32 * c, o);
+                    tmem_wait_ld();
+                    reg_tie<32>(o);
 #pragma unroll
-                for (int j = 0; j < 32; j += 2)
-                    o[j / 2] = bad ? 0u : pack_bf16(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv);
-                if (row < rows) {
+                    for (int j = 0; j < 32; j += 2)
+                        o[j / 2] = bad ? 0u : pack_bf16(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv);
+                    if (row < rows) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        *reinterpret_cast<uint4*>(dst + 32 * c + 8 * k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        for (int k = 0; k < 4; ++k)
+                            *reinterpret_cast<uint4*>(dst + 32 * c + 8 * k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    }
+                }
+            } else {
+                // ---------------------------------------------------- the join of the parts
+                // Every part's maximum m and sum l of a row, its O scaled to the common
+                // maximum in shared memory (the operands there are done with), then each
+                // part sums 1 / splits of the columns over the parts, in their order.
+                constexpr int ROWS = 128 * C::MT;
+                float2* stat = reinterpret_cast<float2*>(sm);                 // [row] (m, l)
+                float4* stage = reinterpret_cast<float4*>(sm + ROWS * 8);     // [four columns][row]
+                static_assert(ROWS * 8 + ROWS * C::VN * 4 <= C::OFF_MISC, "the stage fits below the barriers");
+                const int tr = g * 128 + r;
+                if (nitems == 0) mbar_wait_warp(&misc.q_full, 0);  // (else the first scores have)
+                named_bar_sync<1, 32 * C::SOFT_WARPS>();  // (no MMA of this CTA reads operands any more)
+                stat[tr] = make_float2(nitems > 0 ? mx : -INFINITY, l);
+                cluster_sync();
+                float top = -INFINITY, total = 0.f;
+                for (int p = 0; p < splits; ++p) {
+                    const float2 v = ld_shared_cluster_f2(map_shared_rank(smem_u32(stat + tr), p * C::NV + rank));
+                    const float t = fmaxf(top, v.x);
+                    if (t != -INFINITY) total = total * ex2(top - t) + v.y * ex2(v.x - t);
+                    top = t;
+                }
+                const float f = nitems > 0 && mx != -INFINITY ? ex2(mx - top) : 0.f;
+#pragma unroll 1
+                for (int c = 0; c < C::VN / 32; ++c) {
+                    uint32_t o[32];
+                    if (f != 0.f || nitems > 0) {
+                        tmem_ld32(o_addr + 32 * c, o);
+                        tmem_wait_ld();
+                        reg_tie<32>(o);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (f != 0.f)
+                            v = make_float4(__uint_as_float(o[j]) * f, __uint_as_float(o[j + 1]) * f, __uint_as_float(o[j + 2]) * f,
+                                            __uint_as_float(o[j + 3]) * f);
+                        stage[(c * 8 + j / 4) * ROWS + tr] = v;
+                    }
+                }
+                cluster_sync();
+                const float inv = a.out_scale / total;
+                const int c0 = C::VN / 4 * split >> log_splits, c1 = C::VN / 4 * (split + 1) >> log_splits;  // groups of four columns
+                for (int c = c0; c < c1; c += 2) {
+                    float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+                    for (int p = 0; p < splits; ++p) {
+                        const uint32_t at = map_shared_rank(smem_u32(stage + c * ROWS + tr), p * C::NV + rank);
+                        const float4 x = ld_shared_cluster_f4(at), y = ld_shared_cluster_f4(at + ROWS * 16);
+                        u.x += x.x, u.y += x.y, u.z += x.z, u.w += x.w;
+                        v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+                    }
+                    uint4 o = make_uint4(pack_bf16(u.x * inv, u.y * inv), pack_bf16(u.z * inv, u.w * inv), pack_bf16(v.x * inv, v.y * inv),
+                                         pack_bf16(v.z * inv, v.w * inv));
+                    if (bad) o = make_uint4(0u, 0u, 0u, 0u);
+                    if (row < rows) *reinterpret_cast<uint4*>(dst + 4 * c) = o;
                 }
             }
             tc_fence_before();
         }
+        if (splits > 1 && (warp < 4 || warp >= 4 + C::SOFT_WARPS)) {  // the softmax warps' meetings in the join
+            cluster_sync();
+            cluster_sync();
+        }
     }
-    if constexpr (C::PAIR) cluster_sync();  // (nothing of this CTA's memory is written any more)
+    __syncwarp();
+    if (cluster > 1) cluster_sync();  // (no other CTA reads or writes this one's memory any more)
     else __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
@@ -694,21 +768,44 @@ cudaError_t launch_cfg(const PrefillArgs& a, cudaStream_t stream) {
         if (regs / 8 * 8 * C::THREADS < 128 * (2 * kSoftRegs + kOtherRegs)) return cudaErrorInvalidConfiguration;
     }
     const long long places = (long long)(q_rows / C::BM) + a.batch;
-    const long long grid = places * a.branches * C::NV;
-    if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    cfg.attrs = attr;
+    // Row blocks in flight at once: one CTA (or pair) per SM.  Where they leave SMs
+    // idle, a row block's tokens are split over a cluster of up to 8 CTAs, four
+    // tiles each at least (by the block table, which bounds the lengths) and as
+    // many clusters as the device holds at once (a cluster stays within a group of
+    // SMs).  One new token after 8191: 28.8 us in 8 parts, 42 in 4, 129 in one;
+    // 4 x 16 tokens after 8192: 48 us in 4 parts, 65 in 8 (two waves), 135 in one.
+    static const auto resident = [&] {
+        std::array<int, 4> n{};  // clusters of 1, 2, 4, 8 CTAs
+        cudaLaunchConfig_t c = cfg;
+        c.numAttrs = 1;
+        for (int k = 0; k < 4; ++k) {
+            attr[0].val.clusterDim = {1u << k, 1, 1};
+            c.gridDim = dim3(1u << k);
+            if (cudaOccupancyMaxActiveClusters(&n[k], kernel, &c) != cudaSuccess) n[k] = 0;
+        }
+        cudaGetLastError();
+        return n;
+    }();
+    const long long blocks = (long long)((q_rows + C::BM - 1) / C::BM) * a.branches;
+    const long long most = (long long)a.max_pages * a.page_size / (4 * C::KT);
+    int log_splits = 0;
+    while (C::NV << log_splits < 8 && blocks <= resident[log_splits + 1 + (C::NV == 2)] && 2 << log_splits <= most) ++log_splits;
+    const long long grid = places * a.branches * C::NV << log_splits;
+    if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+    cfg.gridDim = dim3((unsigned)grid);
+    attr[0].val.clusterDim = {(unsigned)(C::NV << log_splits), 1, 1};
+    attr[1] = attr[0];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {C::NV, 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = C::PAIR ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, maps, a, places);
+    cfg.numAttrs = C::NV << log_splits > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, maps, a, places, log_splits);
 }
 
 template <int DC>

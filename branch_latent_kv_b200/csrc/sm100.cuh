@@ -444,6 +444,12 @@ __device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ float2 ld_shared_cluster_f2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
 // Arrives on a barrier of another CTA of the cluster (address from
 // map_shared_rank); what this thread read and wrote before is ordered before it.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote_bar) {

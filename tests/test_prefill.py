@@ -91,6 +91,50 @@ def test_lengths_around_the_tiles(new, past, branches, d_c, heads):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("branches,d_c", SHAPES)
+@pytest.mark.parametrize("heads,new,past", [(16, [3], [5000]), (1, [300], [3000]), (5, [1, 2], [2100, 40]), (16, [40, 0, 7], [1500, 9, 2600])])
+def test_few_rows_over_long_contexts(branches, d_c, heads, new, past):
+    """Row blocks that leave most SMs idle: their tokens are split over
+    clusters; parts without tiles, and parts that some rows see nothing of."""
+    c = _case(17, heads, branches, d_c, 64, 64, new, past)
+    _check(c, f"H={heads} new={new} past={past}")
+
+
+@pytest.mark.gpu
+def test_chunks_split_for_the_last_wave():
+    """More row blocks than SMs, contexts several times the chunks: two parts
+    each; against the same call's rows one sequence at a time."""
+    c = _case(18, 16, 4, 64, 32, 64, [160] * 4, [900, 700, 800, 1100], poison=False)
+    got = _check(c)
+    for n in range(4):
+        lo, hi = int(c["cu_seqlens"][n]), int(c["cu_seqlens"][n + 1])
+        d = {**c, "q_lat": c["q_lat"][lo:hi].contiguous(), "q_rope": c["q_rope"][lo:hi].contiguous(), "block_table": c["block_table"][n:n + 1].contiguous(),
+             "seqlens": c["seqlens"][n:n + 1].clone(), "cu_seqlens": torch.tensor([0, hi - lo], dtype=torch.int32)}
+        ref.within(b.mlra_prefill(**_gpu(d)), got[lo:hi].double().cpu(), 2.0 ** -6 * got[lo:hi].double().abs().cpu() + 2.0 ** -8 * float(got.abs().max()))
+
+
+@pytest.mark.gpu
+def test_bad_page_behind_a_split():
+    """A page outside the pool in one part's tokens empties every part's rows."""
+    c = _case(19, 8, 4, 128, 64, 64, [4, 3], [4000, 20])
+    out, tol = _expect(c)
+    c["block_table"][0, 10] = -7
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = b.mlra_prefill(**_gpu(c), device_status=status)
+    assert int(status.item()) == b.MLRA_ERR_DEVICE_BAD_INDEX
+    assert bool((got[:4] == 0).all())
+    ref.within(got[4:], out[4:], tol[4:])
+
+
+@pytest.mark.gpu
+def test_zero_and_negative_scales():
+    for scale in (0.0, -0.05):
+        c = _case(20, 8, 2, 128, 64, 64, [130], [70])
+        c["scale"] = scale
+        _check(c, f"scale {scale}")
+
+
+@pytest.mark.gpu
 def test_long_prompt_of_the_benchmark_shape():
     c = _case(4, 16, 4, 128, 64, 64, [1200], [300])
     _check(c)

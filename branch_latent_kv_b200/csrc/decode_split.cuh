@@ -186,10 +186,10 @@ __device__ __forceinline__ int first_len(const DecodeArgs& a, int n) {
 
 template <int SEQ = kSeqCost>
 __device__ __forceinline__ bool next_segment(const DecodeArgs& a, int& n, int& cum, int A0, int A1,
-                                             int& L, int& tiles, int& tb, int& te, int& next_len) {
-    while (n < a.batch && cum < A1) {
+                                             int& L, int& tiles, int& tb, int& te, int& next_len, int end) {
+    while (n < end && cum < A1) {
         L = next_len;
-        next_len = n + 1 < a.batch ? __ldg(a.seqlens + n + 1) : 0;
+        next_len = n + 1 < end ? __ldg(a.seqlens + n + 1) : 0;
         tiles = seq_tiles(L, a.page_size, a.max_pages);
         if (tiles > 0) {
             tb = first_tile_at(cum, tiles, A0);
@@ -200,6 +200,10 @@ __device__ __forceinline__ bool next_segment(const DecodeArgs& a, int& n, int& c
         ++n;
     }
     return false;
+}
+__device__ __forceinline__ bool next_segment(const DecodeArgs& a, int& n, int& cum, int A0, int A1,
+                                             int& L, int& tiles, int& tb, int& te, int& next_len) {
+    return next_segment<kSeqCost>(a, n, cum, A0, A1, L, tiles, tb, te, next_len, a.batch);
 }
 
 template <int SEQ = kSeqCost>

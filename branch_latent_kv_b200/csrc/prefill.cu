@@ -165,24 +165,34 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return r;
 }
 
-// Row blocks ("places") of sequence n start at cu[n] H / BM + n: room for
-// ceil(q H / BM) of them.  In 64 bits, since cu may hold anything.
-__device__ __forceinline__ long long place_of(const PrefillArgs& a, int n, int BM) {
-    const long long rows = (long long)__ldg(a.cu_seqlens + n) * a.heads;
+// Row blocks ("places") of sequence n, whose offset is c0, start at c0 H / BM +
+// n: room for ceil(q H / BM) of them.  In 64 bits, since c0 may be anything.
+__device__ __forceinline__ long long place_of(int c0, int n, int heads, int BM) {
+    const long long rows = (long long)c0 * heads;
     return (rows >= 0 ? rows / BM : -((BM - 1 - rows) / BM)) + n;
 }
 
-// Whole warp: the last sequence whose first place is at or before v.
-__device__ __forceinline__ int find_seq(const PrefillArgs& a, long long v, int BM) {
+// Whole warp: the last sequence whose first place is at or before v, its
+// offsets and length (the last round loads them with what it searches).
+__device__ __forceinline__ int find_seq(const PrefillArgs& a, long long v, int BM, int& c0, int& c1, int& L) {
     const int lane = threadIdx.x & 31;
     int lo = 0, len = a.batch;  // the answer lies in [lo, lo + len)
-    while (len > 1) {
+    while (len > 32) {
         const int step = (len + 31) / 32, n = lo + lane * step, end = lo + len;
-        const unsigned hit = __ballot_sync(0xffffffffu, n < end && place_of(a, n, BM) <= v);
+        const unsigned hit = __ballot_sync(0xffffffffu, n < end && place_of(__ldg(a.cu_seqlens + n), n, a.heads, BM) <= v);
         lo += (hit ? 31 - __clz(hit) : 0) * step;
         len = min(step, end - lo);
     }
-    return lo;
+    const int n = lo + min(lane, len - 1);
+    c0 = __ldg(a.cu_seqlens + n);
+    c1 = __ldg(a.cu_seqlens + n + 1);
+    L = __ldg(a.seqlens + n);
+    const unsigned hit = __ballot_sync(0xffffffffu, lane < len && place_of(c0, n, a.heads, BM) <= v);
+    const int k = hit ? 31 - __clz(hit) : 0;
+    c0 = __shfl_sync(0xffffffffu, c0, k);
+    c1 = __shfl_sync(0xffffffffu, c1, k);
+    L = __shfl_sync(0xffffffffu, L, k);
+    return lo + k;
 }
 
 template <int DR>
@@ -213,7 +223,9 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
     const long long place = places - 1 - job / B;
 
     launch_dependents();
-    if (threadIdx.x == 32) {
+    // warp 0 sets up the barriers, finds the row block and requests its queries;
+    // the others meet it then
+    if (threadIdx.x == 0) {
         for (int i = 0; i < C::NC; ++i) mbar_init(&misc.c_full[i], 1), mbar_init(&misc.c_empty[i], 1);
         for (int i = 0; i < C::NK; ++i) mbar_init(&misc.k_full[i], 1), mbar_init(&misc.k_empty[i], 1);
         for (int i = 0; i < 2; ++i) {
@@ -235,16 +247,15 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
         fence_barrier_init();
     }
     if (warp == 1) {
-        __syncwarp();
         tmem_alloc(&misc.tmem_base, C::TMEM_COLS);
         tmem_relinquish();
     }
     wait_prerequisite_grid();
     if (warp == 0) {
-        const int n = find_seq(a, place, C::BM);
-        const int c0 = __ldg(a.cu_seqlens + n), c1 = __ldg(a.cu_seqlens + n + 1), L = __ldg(a.seqlens + n);
+        int c0, c1, L;
+        const int n = find_seq(a, place, C::BM, c0, c1, L);
         const bool run = c0 >= 0 && c1 >= c0 && c1 <= a.tokens;
-        const long long row0 = (place - place_of(a, n, C::BM)) * C::BM;
+        const long long row0 = (place - place_of(c0, n, H, C::BM)) * C::BM;
         const bool mine = run && row0 >= 0 && row0 < (long long)(c1 - c0) * H;
         const bool good = L >= c1 - c0 && seqlen_valid(L, P, a.max_pages);
         if (lane == 0) {
@@ -254,6 +265,15 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             misc.job[3] = mine ? c0 * H : 0;
             misc.job[4] = good ? L - (c1 - c0) : -1;
             if (mine && !good && a.status != nullptr) record_error(a.status, MLRA_ERR_DEVICE_BAD_SEQLEN);
+            if (mine && good) {
+                mbar_arrive_expect_tx(&misc.q_full, C::MT * (C::Q_LAT + (has_rope ? C::QR_BYTES : 0)));
+                for (int m = 0; m < C::MT; ++m) {
+                    uint8_t* dst = sm + C::OFF_Q + m * C::Q_TILE;
+                    const int y = c0 * H + (int)row0 + m * 128;
+                    for (int c = 0; !C::QT && c < C::NCH; ++c) tma_load_2d(dst + c * C::Q_CHUNK, &maps.q, col0 + c * 64, y, &misc.q_full);
+                    if (has_rope) tma_load_2d(dst + C::Q_LAT, &maps.qr, rope0, y, &misc.q_full);
+                }
+            }
         }
     }
     tc_fence_before();
@@ -293,16 +313,6 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             // ------------------------------------------------------------ copies
             const int box = min(P, C::KT);
             bool ok = true;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&misc.q_full, C::MT * (C::Q_LAT + (has_rope ? C::QR_BYTES : 0)));
-                for (int m = 0; m < C::MT; ++m) {
-                    uint8_t* dst = sm + C::OFF_Q + m * C::Q_TILE;
-                    const int y = (int)out0 + m * 128;
-                    for (int c = 0; !C::QT && c < C::NCH; ++c)
-                        tma_load_2d(dst + c * C::Q_CHUNK, &maps.q, col0 + c * 64, y, &misc.q_full);
-                    if (has_rope) tma_load_2d(dst + C::Q_LAT, &maps.qr, rope0, y, &misc.q_full);
-                }
-            }
             int win = t0 * C::KT / P, page_of_lane = 0;  // 32 block-table entries from `win` on
             if (win + lane < a.max_pages) page_of_lane = __ldg(bt + win + lane);
             int done = 0;  // tiles whose copies were issued

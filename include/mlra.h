@@ -317,7 +317,8 @@ MLRA_API mlra_status mlra_prepare(const mlra_dims* dims, int32_t d_h, const void
  *                L < max(q, 1) or beyond the block table (rows written as
  *                zeros), or offsets that decrease or leave [0, T] (no rows
  *                written); MLRA_ERR_DEVICE_BAD_INDEX: a page of the sequence
- *                outside the pool (rows written as zeros).
+ *                outside the pool (rows written as zeros);
+ *                MLRA_ERR_DEVICE_TIMEOUT: a bounded wait expired (zeros).
  * Cache slots at or behind L never reach a result, whatever they hold; a
  * non-finite latent before L reaches the rows of its sequence.
  * Scores, maxima and sums are fp32; the probabilities enter the output
@@ -380,10 +381,13 @@ MLRA_API mlra_status mlra_append_fp8(const mlra_dims* dims, int32_t tokens, cons
  * mlra_decode over the 8-bit cache: the same arguments, shapes, workspace and
  * errors, with
  *   latent_cache e4m3 [num_pages, page_size, branches, d_c]
- *   latent_scale fp32 [num_pages, page_size / 16, branches], positive and
- *                finite (mlra_append_fp8 writes powers of two)
+ *   latent_scale fp32 [num_pages, page_size / 16, branches]: positive, finite
+ *                and not subnormal for the blocks of the sequences
+ *                (mlra_append_fp8 writes powers of two from 2^-40 on)
  * The queries, scores, sums and outputs keep mlra_decode's precision: only
- * the cache is in 8 bits.
+ * the cache is in 8 bits.  (Queries enter the products as two e4m3 parts, 2^-17
+ * of the sequence's largest query value; probabilities as three e5m2 parts,
+ * 2^-9 of each.)
  */
 MLRA_API mlra_status mlra_decode_fp8(const mlra_dims* dims, const void* q_lat, const void* q_rope,
                                      const void* latent_cache, const void* latent_scale, const void* rope_cache,

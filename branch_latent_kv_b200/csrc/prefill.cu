@@ -11,13 +11,15 @@
 //   S = [Q | Qr] [C | Kr]^T,  O += P C,
 // rows r = i H + h lying in memory at a constant stride whatever H is.
 //
-// One CTA per (128 MT rows of a sequence, branch, VN value columns):
-//   warp 0     copies: Q once, then per tile of KT tokens the latents and the
+// One CTA per (128 MT rows of a sequence, branch), or, for d_c = 512, a pair:
+//   warp 0     finds the CTA's row blocks, one after the other, and copies: Q
+//              once a block, then per tile of KT tokens the latents and the
 //              keys (one TMA box per page, or part of one) into two rings
 //   warp 1     MMAs (tcgen05, one elected thread) and TMEM:
 //                S[slot] = Q C^T + Qr Kr^T   K = d_c + d_r, N = KT
 //                O += P[slot] C              P from TMEM, the same tile of C as
 //                                            MN-major operand, N = VN
+//   warp 2     the sequence's pages: all in the pool?
 //   warps 4..  softmax, one thread per row (a TMEM lane): one pass with a
 //              running maximum and sum; P goes to TMEM as bf16 over the
 //              scores it came from; at the end O / sum is written
@@ -28,6 +30,40 @@
 // because MMAs run in issue order the slot needs no further barrier.
 // The running maximum is raised only when a score exceeds it by 2^8 (a row's
 // O is rescaled then, by the row's own warp, without a barrier between warps).
+//
+// The grid has a CTA for each row block, but one that has issued its last copy
+// takes the place of one that has not started (cluster launch control): the
+// next block's queries, first tiles and first scores come while this one's
+// last softmax and its output are under way.  Prompts of 1 to 1024 tokens, 612
+// blocks: 54 us against 67 with a new CTA for every block.
+//
+// What the widths ask for, with what it measured:
+//  - d_c <= 128: tiles of 128 x 128 scores, a row of them in one thread's
+//    registers: the softmax warpgroups take registers from the first one.
+//  - d_c >= 256: the latent queries live in TMEM (operand A of the score MMA),
+//    so shared memory holds latents only, up to four tiles of 64 tokens in flight.
+//  - d_c = 512: a row's output does not fit TMEM beside the scores, and two CTAs
+//    that each compute all scores for half of the output do 1.5 times the
+//    products, out of smaller tiles.  A pair divides the columns for both instead:
+//    each CTA has the partial scores of its 256 columns and sends them to the
+//    other (st.async to its shared memory), the softmax adds the two.  Two
+//    prompts of 3937 tokens together, 16 heads: 603 us with all scores computed
+//    twice, 319 as a pair, 252 with the queries in TMEM and the scores sent by
+//    warps of their own (8 to 11).
+//  - few row blocks: a cluster of up to 8 CTAs divides a block's tokens, and
+//    joins outputs, maxima and sums over distributed shared memory (one new
+//    token after 8191 of four 128-wide branches: 28 us against 129).
+//
+// Bound by (a rate counts the masked half of the diagonal tiles as nothing):
+//  - d_c = 128, 8192 tokens of 16 heads and four branches: 1.09 PFLOP/s in short
+//    runs (1073 us), 0.93 under the power cap.  An item's softmax (128 scores a
+//    thread, their exponentials on the special-function units) takes 1900 to
+//    2600 cycles, its MMAs 1280 and a pair of items 4550: the two warpgroups
+//    of a scheduler share its issue slots.
+//  - d_c = 512: 2900 cycles per 64 tokens, of which the products are 1500: the
+//    exchange of the partial scores is a chain of TMEM read, store, add.
+//  - short prompts: 6 us of dependent reads before an SM's first product, its
+//    blocks' outputs, and the spread of the SMs' last blocks.
 //
 // P is rounded to bf16 (the output MMA takes P and C in one type, and C is
 // bf16): half a step, 2^-8 of each probability, averaged over the row; the
@@ -100,6 +136,14 @@ struct Cfg {
 constexpr int kSoftRegs = 200, kOtherRegs = 104;
 static_assert(128 * (2 * kSoftRegs + kOtherRegs) <= 3 * 128 * 168, "the split fits the launch");
 
+// A row block: sequence (-1: no more), first row in it, rows, first packed row,
+// tokens before the new ones (-1: zeros), branch, tokens that some row sees; the
+// tiles and the row blocks with queries that this CTA had before it.
+struct Job {
+    int n, row0, rows, out0, past, b, kv_end;
+    uint32_t tiles, asked;
+};
+
 struct Misc {
     uint64_t c_full[4], c_empty[4];
     uint64_t k_full[4], k_empty[4];
@@ -111,12 +155,16 @@ struct Misc {
     // are read there; this CTA's are read out of TMEM for sending
     uint64_t x_full[2], x_read[2], x_empty[2], x_taken[2];
     uint64_t q_tmem;  // QT: the latent queries are in TMEM
-    uint64_t q_full;
+    uint64_t q_full, q_empty;  // the queries in shared memory; every score MMA of the row block has read them
+    // row block k of this CTA in place k % 2: it is known; its pages are checked; every reader is done with it
+    uint64_t job_full[2], checked[2], job_empty[2];
+    uint64_t next_full;
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
-    int bad;      // a page of the sequence lies outside the pool
-    int job[5];   // sequence (-1: none), first row in it, rows, first packed row, past (-1: zeros)
+    int bad[2];  // a page of the sequence lies outside the pool
+    Job job[2];
+    alignas(16) uint32_t next[4];  // the answer to a request for another CTA's place
 };
 
 struct Maps {
@@ -195,6 +243,25 @@ __device__ __forceinline__ int find_seq(const PrefillArgs& a, long long v, int B
     return lo + k;
 }
 
+// Takes the place of a CTA that has not started: its index, or -1 when none is
+// left (then no other request may follow).
+__device__ __forceinline__ void request_place(uint32_t* answer, uint64_t* bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                 ::"r"(smem_u32(answer)), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ int place_taken(const uint32_t* answer) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n.reg .pred p;\n.reg .b128 h;\n"
+        "ld.shared.b128 h, [%2];\n"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n"
+        "selp.u32 %0, 1, 0, p;\n"
+        "mov.u32 %1, 0;\n"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, _, _, _}, h;\n}"
+        : "=r"(got), "=r"(x) : "r"(smem_u32(answer)) : "memory");
+    return got ? (int)x : -1;
+}
+
 template <int DR>
 __device__ __forceinline__ uint64_t rope_desc(uint32_t addr) {
     return DR == 64 ? smem_desc(addr, 16, 1024, kLayoutSw128) : smem_desc(addr, 16, 512, kLayoutSw64);
@@ -214,17 +281,65 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
     // a cluster: the `splits` parts of a row block's tokens, each a CTA or a pair
     const int splits = 1 << log_splits, cluster = splits * C::NV;
     const int crank = blockIdx.x & (cluster - 1), split = crank / C::NV, rank = crank % C::NV;
-    const uint32_t job = blockIdx.x / C::NV >> log_splits;
-    const int b = job % B;
-    const int col0 = b * DC + rank * C::DL;  // this CTA's first column of a latent row
     const bool has_rope = !C::PAIR || DR == 64 || rank == 0;
     const int rope0 = C::PAIR && DR == 64 ? rank * C::RL : 0;  // its first RoPE column
-    // a sequence's later row blocks see more tokens: they start first
-    const long long place = places - 1 - job / B;
+    const size_t W = (size_t)B * DC;
+    volatile int* abort_flag = &misc.abort_flag;
+    // this CTA's tiles of a row block: [t0, t0 + ntiles) of all (none where there
+    // are fewer than parts)
+    auto span = [&](const Job& job, int& t0, int& ntiles) {
+        const int all_tiles = ceil_div(job.kv_end, C::KT);
+        t0 = all_tiles * split >> log_splits;  // (at most 2^25 tiles, 8 parts)
+        ntiles = (all_tiles * (split + 1) >> log_splits) - t0;
+    };
+    // row block k of this CTA, once it is known
+    auto job_at = [&](uint32_t k, Job& job) {
+        const bool ok = mbar_wait_warp(&misc.job_full[k & 1], (k >> 1) & 1);
+        job = misc.job[k & 1];
+        return ok;
+    };
+    auto job_done = [&](uint32_t k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&misc.job_empty[k & 1]);
+    };
+    // warp 0: the row block of place `id` becomes row block k, its queries are
+    // requested; false: the place has none
+    Job mine;
+    bool ok0 = true;
+    auto take = [&](uint32_t id, uint32_t k, uint32_t tiles, uint32_t asked) {
+        const int b = id % B;
+        const long long place = places - 1 - id / B;  // a sequence's later row blocks see more tokens: they start first
+        int c0, c1, L;
+        const int n = find_seq(a, place, C::BM, c0, c1, L);
+        const bool run = c0 >= 0 && c1 >= c0 && c1 <= a.tokens;
+        const long long row0 = (place - place_of(c0, n, H, C::BM)) * C::BM;
+        if (!run || row0 < 0 || row0 >= (long long)(c1 - c0) * H) return false;
+        const bool good = L >= c1 - c0 && seqlen_valid(L, P, a.max_pages);
+        const int rows = (c1 - c0) * H, past = L - (c1 - c0);
+        mine = Job{n, (int)row0, rows, c0 * H, good ? past : -1, b, past + (min((int)row0 + C::BM, rows) - 1) / H + 1, tiles, asked};
+        if (lane == 0) {
+            misc.job[k & 1] = mine;
+            mbar_arrive(&misc.job_full[k & 1]);
+            if (!good && a.status != nullptr) record_error(a.status, MLRA_ERR_DEVICE_BAD_SEQLEN);
+        }
+        if (!good) return true;
+        if (asked > 0) ok0 = mbar_wait_warp(&misc.q_empty, (asked - 1) & 1);
+        if (ok0 && lane == 0) {
+            mbar_arrive_expect_tx(&misc.q_full, C::MT * (C::Q_LAT + (has_rope ? C::QR_BYTES : 0)));
+            for (int m = 0; m < C::MT; ++m) {
+                uint8_t* dst = sm + C::OFF_Q + m * C::Q_TILE;
+                const int y = c0 * H + (int)row0 + m * 128;
+                for (int c = 0; !C::QT && c < C::NCH; ++c)
+                    tma_load_2d(dst + c * C::Q_CHUNK, &maps.q, b * DC + rank * C::DL + c * 64, y, &misc.q_full);
+                if (has_rope) tma_load_2d(dst + C::Q_LAT, &maps.qr, rope0, y, &misc.q_full);
+            }
+        }
+        return true;
+    };
 
     launch_dependents();
-    // warp 0 sets up the barriers, finds the row block and requests its queries;
-    // the others meet it then
+    // warp 0 sets up the barriers, finds the first row block and requests its
+    // queries; the others meet it then
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NC; ++i) mbar_init(&misc.c_full[i], 1), mbar_init(&misc.c_empty[i], 1);
         for (int i = 0; i < C::NK; ++i) mbar_init(&misc.k_full[i], 1), mbar_init(&misc.k_empty[i], 1);
@@ -241,9 +356,16 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
         }
         mbar_init(&misc.q_tmem, 4);
         mbar_init(&misc.q_full, 1);
+        mbar_init(&misc.q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&misc.job_full[i], 1);
+            mbar_init(&misc.checked[i], 1);
+            mbar_init(&misc.job_empty[i], 2 + C::SOFT_WARPS);  // the MMA warp, the page check, the softmax warps
+        }
+        mbar_init(&misc.next_full, 1);
         mbar_init(&misc.drain, 1);
         misc.abort_flag = 0;
-        misc.bad = 0;
+        misc.job[0].n = -1;
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -251,361 +373,324 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
         tmem_relinquish();
     }
     wait_prerequisite_grid();
-    if (warp == 0) {
-        int c0, c1, L;
-        const int n = find_seq(a, place, C::BM, c0, c1, L);
-        const bool run = c0 >= 0 && c1 >= c0 && c1 <= a.tokens;
-        const long long row0 = (place - place_of(c0, n, H, C::BM)) * C::BM;
-        const bool mine = run && row0 >= 0 && row0 < (long long)(c1 - c0) * H;
-        const bool good = L >= c1 - c0 && seqlen_valid(L, P, a.max_pages);
-        if (lane == 0) {
-            misc.job[0] = mine ? n : -1;
-            misc.job[1] = mine ? (int)row0 : 0;
-            misc.job[2] = mine ? (c1 - c0) * H : 0;
-            misc.job[3] = mine ? c0 * H : 0;
-            misc.job[4] = good ? L - (c1 - c0) : -1;
-            if (mine && !good && a.status != nullptr) record_error(a.status, MLRA_ERR_DEVICE_BAD_SEQLEN);
-            if (mine && good) {
-                mbar_arrive_expect_tx(&misc.q_full, C::MT * (C::Q_LAT + (has_rope ? C::QR_BYTES : 0)));
-                for (int m = 0; m < C::MT; ++m) {
-                    uint8_t* dst = sm + C::OFF_Q + m * C::Q_TILE;
-                    const int y = c0 * H + (int)row0 + m * 128;
-                    for (int c = 0; !C::QT && c < C::NCH; ++c) tma_load_2d(dst + c * C::Q_CHUNK, &maps.q, col0 + c * 64, y, &misc.q_full);
-                    if (has_rope) tma_load_2d(dst + C::Q_LAT, &maps.qr, rope0, y, &misc.q_full);
-                }
-            }
-        }
-    }
+    const uint32_t first = blockIdx.x / C::NV >> log_splits;
+    bool have = false;
+    if (warp == 0) have = take(first, 0, 0, 0);
     tc_fence_before();
     if (cluster > 1) cluster_sync();  // (the other CTAs' barriers are set up too)
     else __syncthreads();
     tc_fence_after();
-    const int n = misc.job[0], row0 = misc.job[1], rows = misc.job[2], past = misc.job[4];
-    const size_t out0 = (size_t)misc.job[3] + row0;  // this CTA's first (token, head) row of out
     const uint32_t tmem = misc.tmem_base;
-    const size_t W = (size_t)B * DC;
-    if (blockIdx.x == 0 && a.status != nullptr) {  // offsets out of range, whichever places they claim
-        for (int m = threadIdx.x; m < a.batch; m += C::THREADS) {
-            const int c0 = __ldg(a.cu_seqlens + m), c1 = __ldg(a.cu_seqlens + m + 1);
-            if (c0 < 0 || c1 < c0 || c1 > a.tokens) record_error(a.status, MLRA_ERR_DEVICE_BAD_SEQLEN);
-        }
+    if constexpr (C::MT == 2) {
+        if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     }
-
-    if (n >= 0 && past < 0) {  // a bad length: zeros
-        const int left = min(C::BM, rows - row0);
-        for (int e = threadIdx.x; e < left * (C::VN / 8); e += C::THREADS)
-            *reinterpret_cast<uint4*>(a.out + (out0 + e / (C::VN / 8)) * W + col0 + e % (C::VN / 8) * 8) =
-                make_uint4(0u, 0u, 0u, 0u);
-    } else if (n >= 0) {
-        const int last_row = min(row0 + C::BM, rows) - 1;
-        const int kv_end = past + last_row / H + 1;  // tokens that some row sees
-        // this CTA's tiles: [t0, t0 + ntiles) of all (none where there are fewer than parts)
-        const int all_tiles = ceil_div(kv_end, C::KT);
-        const int t0 = all_tiles * split >> log_splits;  // (at most 2^25 tiles, 8 parts)
-        const int ntiles = (all_tiles * (split + 1) >> log_splits) - t0, nitems = ntiles * C::MT;
-        const int32_t* bt = a.block_table + (size_t)n * a.max_pages;
-        volatile int* abort_flag = &misc.abort_flag;
-
-        if constexpr (C::MT == 2) {
-            if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        }
-        if (warp == 0) {
-            // ------------------------------------------------------------ copies
-            const int box = min(P, C::KT);
-            bool ok = true;
-            int win = t0 * C::KT / P, page_of_lane = 0;  // 32 block-table entries from `win` on
-            if (win + lane < a.max_pages) page_of_lane = __ldg(bt + win + lane);
-            int done = 0;  // tiles whose copies were issued
-            for (int i = 0; i < ntiles && ok; ++i) {
-                const int tok0 = (t0 + i) * C::KT, nbox = ceil_div(min(C::KT, kv_end - tok0), box);
-                const int page0 = tok0 / P;
-                if (page0 + (nbox * box + P - 1) / P > win + 32) {
-                    win = page0;
-                    page_of_lane = win + lane < a.max_pages ? __ldg(bt + win + lane) : 0;
-                }
-                const int cs = i % C::NC, ks = i % C::NK;
-                if (lane == 0) {
-                    if (i >= C::NK) ok = mbar_wait(&misc.k_empty[ks], (i / C::NK - 1) & 1);
-                    if (ok && i >= C::NC) ok = mbar_wait(&misc.c_empty[cs], (i / C::NC - 1) & 1);
-                    ok = ok && !*abort_flag;
-                    if (ok) {
-                        mbar_arrive_expect_tx(&misc.k_full[ks], has_rope ? nbox * box * C::RL * 2 : 0);
-                        mbar_arrive_expect_tx(&misc.c_full[cs], nbox * box * C::NCH * 128);
+    if (warp == 0) {
+        // ------------------------------------------------------------ copies
+        const int box = min(P, C::KT);
+        uint32_t blocks = 0, asked = 0, done = 0, requests = 0;  // row blocks, of them with queries; tiles whose copies were issued
+        bool ok = true;
+        for (uint32_t id = first;;) {
+            if (have) ++blocks;
+            if (have && mine.past >= 0) {
+                ++asked;
+                ok = ok0;
+                int t0, ntiles;
+                span(mine, t0, ntiles);
+                const int col0 = mine.b * DC + rank * C::DL;
+                const int32_t* bt = a.block_table + (size_t)mine.n * a.max_pages;
+                int win = t0 * C::KT / P, page_of_lane = 0;  // 32 block-table entries from `win` on
+                if (win + lane < a.max_pages) page_of_lane = __ldg(bt + win + lane);
+                for (int i = 0; i < ntiles && ok; ++i) {
+                    const int tok0 = (t0 + i) * C::KT, nbox = ceil_div(min(C::KT, mine.kv_end - tok0), box);
+                    const int page0 = tok0 / P;
+                    if (page0 + (nbox * box + P - 1) / P > win + 32) {
+                        win = page0;
+                        page_of_lane = win + lane < a.max_pages ? __ldg(bt + win + lane) : 0;
                     }
-                }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) break;
-                for (int q = 0; q < nbox; ++q) {
-                    const int tok = tok0 + q * box;
-                    int page = __shfl_sync(0xffffffffu, page_of_lane, tok / P - win);
-                    page = page >= 0 && page < a.num_pages ? page : 0;  // (the softmax warps report it)
-                    const int y = page * P + tok % P;
+                    const uint32_t cs = done % C::NC, ks = done % C::NK;
                     if (lane == 0) {
-                        if (has_rope)
-                            tma_load_2d(sm + C::OFF_K + ks * C::K_BYTES + q * box * C::RL * 2, &maps.rope, rope0, y, &misc.k_full[ks]);
-                        for (int c = 0; c < C::NCH; ++c)
-                            tma_load_2d(sm + C::OFF_C + cs * C::C_BYTES + c * C::C_CHUNK + q * box * 128, &maps.lat,
-                                        col0 + c * 64, y, &misc.c_full[cs]);
+                        if (done >= C::NK) ok = mbar_wait(&misc.k_empty[ks], (done / C::NK - 1) & 1);
+                        if (ok && done >= C::NC) ok = mbar_wait(&misc.c_empty[cs], (done / C::NC - 1) & 1);
+                        ok = ok && !*abort_flag;
+                        if (ok) {
+                            mbar_arrive_expect_tx(&misc.k_full[ks], has_rope ? nbox * box * C::RL * 2 : 0);
+                            mbar_arrive_expect_tx(&misc.c_full[cs], nbox * box * C::NCH * 128);
+                        }
                     }
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) break;
+                    for (int q = 0; q < nbox; ++q) {
+                        const int tok = tok0 + q * box;
+                        int page = __shfl_sync(0xffffffffu, page_of_lane, tok / P - win);
+                        page = page >= 0 && page < a.num_pages ? page : 0;  // (the page check reports it)
+                        const int y = page * P + tok % P;
+                        if (lane == 0) {
+                            if (has_rope)
+                                tma_load_2d(sm + C::OFF_K + ks * C::K_BYTES + q * box * C::RL * 2, &maps.rope, rope0, y, &misc.k_full[ks]);
+                            for (int c = 0; c < C::NCH; ++c)
+                                tma_load_2d(sm + C::OFF_C + cs * C::C_BYTES + c * C::C_CHUNK + q * box * 128, &maps.lat,
+                                            col0 + c * 64, y, &misc.c_full[cs]);
+                        }
+                    }
+                    ++done;
                 }
-                done = i + 1;
             }
+            if (id == 0 && a.status != nullptr) {  // offsets out of range, whichever places they claim
+                for (int m = lane; m < a.batch; m += 32) {
+                    const int c0 = __ldg(a.cu_seqlens + m), c1 = __ldg(a.cu_seqlens + m + 1);
+                    if (c0 < 0 || c1 < c0 || c1 > a.tokens) record_error(a.status, MLRA_ERR_DEVICE_BAD_SEQLEN);
+                }
+                __syncwarp();
+            }
+            if (!ok || C::PAIR || cluster > 1) break;
+            // the place of a CTA that has not started, asked for when this row block's
+            // last copy is under way
             if (lane == 0) {
-                if (!ok) *abort_flag = 1;
-                // no copy may land after this CTA has gone
-                mbar_wait(&misc.q_full, 0, 200000000ull);
-                for (int i = max(0, done - C::NK); i < done; ++i)
-                    mbar_wait(&misc.k_full[i % C::NK], (i / C::NK) & 1, 200000000ull);
-                for (int i = max(0, done - C::NC); i < done; ++i)
-                    mbar_wait(&misc.c_full[i % C::NC], (i / C::NC) & 1, 200000000ull);
+                fence_proxy_async_smem();  // (the answer before this one has been read)
+                mbar_arrive_expect_tx(&misc.next_full, 16);
+                request_place(misc.next, &misc.next_full);
             }
-        } else if (warp == 1) {
-            // ------------------------------------------------------------ MMAs
-            constexpr uint32_t ID_S = idesc_bf16_f32(128, C::KT, false, false);
-            constexpr uint32_t ID_O = idesc_bf16_f32(128, C::VN, false, true);
-            const uint32_t base = smem_u32(sm);
-            const uint64_t dQ = smem_desc(base + C::OFF_Q, 16, 1024, kLayoutSw128);
-            const uint64_t dQr = rope_desc<C::RL>(base + C::OFF_Q + C::Q_LAT);
-            const uint64_t dC = smem_desc(base + C::OFF_C, 16, 1024, kLayoutSw128);           // K-major
-            const uint64_t dV = smem_desc(base + C::OFF_C, C::C_CHUNK, 1024, kLayoutSw128);  // MN-major
-            const uint64_t dK = rope_desc<C::RL>(base + C::OFF_K);
-            // (one warp's dependent instructions take four cycles and more each:
-            // ring positions are counted, not divided, and the two tiles unrolled)
-            struct Ring {
-                uint32_t at = 0, phase = 0;
-                __device__ __forceinline__ void next(uint32_t depth) {
-                    if (++at == depth) at = 0, phase ^= 1;
-                }
-            };
-            Ring c_new, k_new, c_old;  // the tile of the next scores (latents, keys); the tile of the next PV
-            auto landed = [&]() { return mbar_wait_warp(&misc.k_full[k_new.at], k_new.phase) && mbar_wait_warp(&misc.c_full[c_new.at], c_new.phase); };
-            auto scores = [&](int m, int slot) {  // the elected thread: S[slot] = Q C^T + Qr Kr^T of the new tile
-                const uint32_t d = tmem + slot * C::S_COLS;
-                const uint64_t qr = dQr + ((m * C::Q_TILE) >> 4), k0 = dK + ((k_new.at * C::K_BYTES) >> 4);
-                const uint64_t q = dQ + ((m * C::Q_TILE) >> 4), c = dC + ((c_new.at * C::C_BYTES) >> 4);
+            ok = mbar_wait_warp(&misc.next_full, requests++ & 1);
+            if (!ok) break;
+            const int next = place_taken(misc.next);
+            __syncwarp();
+            if (next < 0) break;
+            id = next;
+            if (blocks >= 2) ok = mbar_wait_warp(&misc.job_empty[blocks & 1], ((blocks >> 1) - 1) & 1);
+            if (!ok) break;
+            have = take(id, blocks, done, asked);
+        }
+        if (ok && blocks >= 2) ok = mbar_wait_warp(&misc.job_empty[blocks & 1], ((blocks >> 1) - 1) & 1);
+        if (lane == 0) {
+            if (ok) {
+                misc.job[blocks & 1].n = -1;  // no more
+                mbar_arrive(&misc.job_full[blocks & 1]);
+            } else {
+                *abort_flag = 1;
+            }
+            // no copy or answer may land after this CTA has gone
+            constexpr uint64_t kLong = 200000000ull;
+            if (asked > 0 && ok0) mbar_wait(&misc.q_full, (asked - 1) & 1, kLong);
+            if (requests > 0) mbar_wait(&misc.next_full, (requests - 1) & 1, kLong);
+            for (uint32_t i = done > C::NK ? done - C::NK : 0; i < done; ++i) mbar_wait(&misc.k_full[i % C::NK], (i / C::NK) & 1, kLong);
+            for (uint32_t i = done > C::NC ? done - C::NC : 0; i < done; ++i) mbar_wait(&misc.c_full[i % C::NC], (i / C::NC) & 1, kLong);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMAs
+        constexpr uint32_t ID_S = idesc_bf16_f32(128, C::KT, false, false);
+        constexpr uint32_t ID_O = idesc_bf16_f32(128, C::VN, false, true);
+        const uint32_t at0 = smem_u32(sm);
+        const uint64_t dQ = smem_desc(at0 + C::OFF_Q, 16, 1024, kLayoutSw128);
+        const uint64_t dQr = rope_desc<C::RL>(at0 + C::OFF_Q + C::Q_LAT);
+        const uint64_t dC = smem_desc(at0 + C::OFF_C, 16, 1024, kLayoutSw128);           // K-major
+        const uint64_t dV = smem_desc(at0 + C::OFF_C, C::C_CHUNK, 1024, kLayoutSw128);  // MN-major
+        const uint64_t dK = rope_desc<C::RL>(at0 + C::OFF_K);
+        // (one warp's dependent instructions take four cycles and more each:
+        // ring positions are counted, not divided, and the two tiles unrolled)
+        struct Ring {
+            uint32_t at = 0, phase = 0;
+            __device__ __forceinline__ void next(uint32_t depth) {
+                if (++at == depth) at = 0, phase ^= 1;
+            }
+        };
+        Ring c_new, k_new, c_old;  // the tile of the next scores (latents, keys); the tile of the next PV
+        auto landed = [&]() { return mbar_wait_warp(&misc.k_full[k_new.at], k_new.phase) && mbar_wait_warp(&misc.c_full[c_new.at], c_new.phase); };
+        auto scores = [&](int m, int slot, bool last) {  // the elected thread: S[slot] = Q C^T + Qr Kr^T of the new tile
+            const uint32_t d = tmem + slot * C::S_COLS;
+            const uint64_t qr = dQr + ((m * C::Q_TILE) >> 4), k0 = dK + ((k_new.at * C::K_BYTES) >> 4);
+            const uint64_t q = dQ + ((m * C::Q_TILE) >> 4), c = dC + ((c_new.at * C::C_BYTES) >> 4);
 #pragma unroll
-                for (int k = 0; k < C::RL / 16; ++k)
-                    if (has_rope) mma_bf16(d, qr + 2 * k, k0 + 2 * k, ID_S, k ? 1u : 0u);
+            for (int k = 0; k < C::RL / 16; ++k)
+                if (has_rope) mma_bf16(d, qr + 2 * k, k0 + 2 * k, ID_S, k ? 1u : 0u);
 #pragma unroll
-                for (int k = 0; k < C::DL / 16; ++k) {
-                    const uint64_t ck = c + ((k / 4 * C::C_CHUNK) >> 4) + k % 4 * 2;
-                    if constexpr (C::QT) mma_bf16_ts(d, tmem + C::Q_COL + 8 * k, ck, ID_S, k || has_rope ? 1u : 0u);
-                    else mma_bf16(d, q + ((k / 4 * C::Q_CHUNK) >> 4) + k % 4 * 2, ck, ID_S, k || has_rope ? 1u : 0u);
-                }
-                mma_commit(&misc.s_full[slot]);
-                if (m == C::MT - 1) mma_commit(&misc.k_empty[k_new.at]);
-            };
-            auto values = [&](int m, int slot, bool first, bool last) {  // the elected thread: O[m] += P[slot] C of the old tile
-                const uint32_t d = tmem + C::O_COL + m * C::VN, p = tmem + slot * C::S_COLS;
-                const uint64_t v = dV + ((c_old.at * C::C_BYTES) >> 4);
+            for (int k = 0; k < C::DL / 16; ++k) {
+                const uint64_t ck = c + ((k / 4 * C::C_CHUNK) >> 4) + k % 4 * 2;
+                if constexpr (C::QT) mma_bf16_ts(d, tmem + C::Q_COL + 8 * k, ck, ID_S, k || has_rope ? 1u : 0u);
+                else mma_bf16(d, q + ((k / 4 * C::Q_CHUNK) >> 4) + k % 4 * 2, ck, ID_S, k || has_rope ? 1u : 0u);
+            }
+            mma_commit(&misc.s_full[slot]);
+            if (m == C::MT - 1) mma_commit(&misc.k_empty[k_new.at]);
+        };
+        auto values = [&](int m, int slot, bool first, bool last) {  // the elected thread: O[m] += P[slot] C of the old tile
+            const uint32_t d = tmem + C::O_COL + m * C::VN, p = tmem + slot * C::S_COLS;
+            const uint64_t v = dV + ((c_old.at * C::C_BYTES) >> 4);
 #pragma unroll
-                for (int k = 0; k < C::KT / 16; ++k) mma_bf16_ts(d, p + 8 * k, v + (k * 2048 >> 4), ID_O, k == 0 && first ? 0u : 1u);
-                if (C::MT == 1 || last) mma_commit(&misc.o_done[slot]);
-                if (m == C::MT - 1) mma_commit(&misc.c_empty[c_old.at]);
-            };
-            bool ok = ntiles == 0 || mbar_wait_warp(&misc.q_full, 0);
-            if constexpr (C::QT) ok = ok && mbar_wait_warp(&misc.q_tmem, 0);
+            for (int k = 0; k < C::KT / 16; ++k) mma_bf16_ts(d, p + 8 * k, v + (k * 2048 >> 4), ID_O, k == 0 && first ? 0u : 1u);
+            if (C::MT == 1 || last) mma_commit(&misc.o_done[slot]);
+            if (m == C::MT - 1) mma_commit(&misc.c_empty[c_old.at]);
+        };
+        bool ok = true;
+        for (uint32_t k = 0; ok; ++k) {
+            Job job;
+            ok = job_at(k, job);
+            if (!ok || job.n < 0) break;
+            job_done(k);
+            if (job.past < 0) continue;
+            int t0, ntiles;
+            span(job, t0, ntiles);
+            ok = ntiles == 0 || mbar_wait_warp(&misc.q_full, job.asked & 1);
+            if constexpr (C::QT) ok = ok && mbar_wait_warp(&misc.q_tmem, job.asked & 1);
             // the first scores: of both row tiles, or of the first two token tiles
 #pragma unroll
             for (int s = 0; s < 2 && ntiles > 0; ++s) {
-                if (s == 0 || C::MT == 1) ok = ok && s < ntiles && landed();
-                if (s > 0 && C::MT == 1 && s >= ntiles) ok = true;  // (one tile only)
-                else if (ok) {
+                const int slot = C::MT == 2 ? s : (job.tiles + s) & 1;
+                if (C::MT == 1 && s >= ntiles) continue;  // (one tile only)
+                if (s == 0 || C::MT == 1) ok = ok && landed();
+                if (ok) {
                     tc_fence_after();
-                    if (elect_one()) scores(C::MT == 2 ? s : 0, s);
+                    if (elect_one()) scores(C::MT == 2 ? s : 0, slot, (C::MT == 2 ? 1 : s + 1) == ntiles);
                     __syncwarp();
                     if (s == C::MT - 1 || C::MT == 1) c_new.next(C::NC), k_new.next(C::NK);
                 }
             }
+            if (ntiles <= (C::MT == 2 ? 1 : 2) && elect_one()) mma_commit(&misc.q_empty);
+            __syncwarp();
             for (int i = 0; i < ntiles && ok; ++i) {
-                const bool more = i + (C::MT == 2 ? 1 : 2) < ntiles;
+                constexpr int AHEAD = C::MT == 2 ? 1 : 2;
+                const bool more = i + AHEAD < ntiles;
                 if (more) ok = landed();
 #pragma unroll
                 for (int m = 0; m < C::MT; ++m) {
-                    const int slot = C::MT == 2 ? m : i & 1;
-                    ok = ok && mbar_wait_warp(&misc.p_full[slot], (C::MT == 2 ? i : i >> 1) & 1);
+                    const uint32_t at = job.tiles + i;
+                    const int slot = C::MT == 2 ? m : at & 1;
+                    ok = ok && mbar_wait_warp(&misc.p_full[slot], (C::MT == 2 ? at : at >> 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
                         values(m, slot, i == 0, i == ntiles - 1);
-                        if (more) scores(m, slot);
+                        if (more) scores(m, slot, i + AHEAD == ntiles - 1);
                     }
                     __syncwarp();
                 }
+                if (i + AHEAD + 1 == ntiles && elect_one()) mma_commit(&misc.q_empty);
+                __syncwarp();
                 c_old.next(C::NC);
-                c_new.next(C::NC);
-                k_new.next(C::NK);
+                if (more) c_new.next(C::NC), k_new.next(C::NK);
                 if ((i & 7) == 7 && __shfl_sync(0xffffffffu, *abort_flag, 0)) ok = false;
             }
-            if (!ok && lane == 0) *abort_flag = 1;
-            // every MMA has finished before TMEM is freed
-            if (elect_one()) mma_commit(&misc.drain);
-            __syncwarp();
-            mbar_wait(&misc.drain, 0, 200000000ull);
-            __syncwarp();
-        } else if (C::PAIR && warp == 3) {
-            // ------------------------------------------------------------ pair: room for the other CTA's scores
-            // (a warp of its own: the arrival over there releases what its thread
-            // wrote, and a thread that has just sent scores waits 1000 cycles for that)
-            bool ok = true;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&misc.x_full[0], C::X_BYTES);
-                mbar_arrive_expect_tx(&misc.x_full[1], C::X_BYTES);
-            }
-            for (int w = 0; w + 2 < nitems; ++w) {
-                ok = mbar_wait_warp(&misc.x_read[w & 1], (w >> 1) & 1);
-                if (!ok) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&misc.x_full[w & 1], C::X_BYTES);
-                    mbar_arrive_cluster(map_shared_rank(smem_u32(&misc.x_empty[w & 1]), crank ^ 1));
-                }
-                __syncwarp();
-            }
-            if (!ok && lane == 0) *abort_flag = 1;
-        } else if (C::PAIR && warp >= 8) {
-            // ------------------------------------------------------------ pair: this CTA's share of the scores
-            // each thread sends its row to the same thread of the other CTA, as
-            // [four tokens][row] of 16 bytes, while the softmax is an item behind
-            const int r = (warp & 3) * 32 + lane;
-            const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-            const uint32_t there = map_shared_rank(smem_u32(sm + C::OFF_X) + r * 16, crank ^ 1);
-            const uint32_t full = map_shared_rank(smem_u32(&misc.x_full[0]), crank ^ 1);
-            bool ok = true;
-            for (int w = 0; w < nitems && ok; ++w) {
-                ok = mbar_wait_warp(&misc.s_full[w & 1], (w >> 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                uint32_t x[C::KT];
-#pragma unroll
-                for (int c = 0; c < C::KT / 32; ++c) tmem_ld32(lanes + (w & 1) * C::S_COLS + 32 * c, x + 32 * c);
-                tmem_wait_ld();
-                reg_tie<C::KT>(x);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&misc.x_taken[w & 1]);
-                if (w >= 2) ok = mbar_wait_warp(&misc.x_empty[w & 1], ((w >> 1) - 1) & 1);
-                if (!ok) break;
-#pragma unroll
-                for (int c = 0; c < C::KT / 4; ++c)
-                    st_async_v4(there + (w & 1) * C::X_BYTES + c * 2048, full + (w & 1) * 8, x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
-            }
-            if (!ok && lane == 0) *abort_flag = 1;
-        } else if (warp >= 4) {
-            // ------------------------------------------------------------ softmax
-            if constexpr (C::MT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-            const int g = (warp - 4) / 4;                 // row tile (MT = 2) of this warpgroup
-            const int quad = warp & 3;                    // TMEM lane quadrant
-            const int r = quad * 32 + lane;               // row within the 128
-            const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-            const uint32_t o_addr = lanes + C::O_COL + g * C::VN;
-            const int row = row0 + g * 128 + r;
-            const int pos = past + min(row, rows - 1) / H;  // last token of this row
-            const int pos_first = past + min(row0 + g * 128 + quad * 32, rows - 1) / H;  // of the warp's first row
-            // (a scale of 0 as 1e-30: every finite score still weighs the same, and a
-            // masked score, infinite, stays so)
-            const float sc = a.scale_log2 == 0.f ? 1e-30f : a.scale_log2;
-            const int L = past + rows / H;
-            if constexpr (C::QT) {
-                // this row's latent queries into TMEM (rows past the last: zeros)
-                const bool real = (long long)out0 + r < (long long)a.tokens * H;
-                const uint4* src = reinterpret_cast<const uint4*>(a.q_lat + (out0 + r) * W + col0);
-#pragma unroll
-                for (int c = 0; c < C::NCH; ++c) {
-                    uint32_t q[32];
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const uint4 v = real ? __ldg(src + 8 * c + u) : make_uint4(0u, 0u, 0u, 0u);
-                        q[4 * u] = v.x, q[4 * u + 1] = v.y, q[4 * u + 2] = v.z, q[4 * u + 3] = v.w;
-                    }
-                    tmem_st32(lanes + C::Q_COL + 32 * c, q);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&misc.q_tmem);
-            }
-            {
-                // every page of the sequence has to lie in the pool
-                bool bad = false;
-                for (int e = threadIdx.x - 128; e < ceil_div(L, P); e += 32 * C::SOFT_WARPS) {
+            if (C::PAIR) break;
+        }
+        if (!ok && lane == 0) *abort_flag = 1;
+        // every MMA has finished before TMEM is freed
+        if (elect_one()) mma_commit(&misc.drain);
+        __syncwarp();
+        mbar_wait(&misc.drain, 0, 200000000ull);
+        __syncwarp();
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ page checks
+        // every page of a row block's sequence has to lie in the pool
+        for (uint32_t k = 0;; ++k) {
+            Job job;
+            if (!job_at(k, job) || job.n < 0) break;
+            bool bad = false;
+            if (job.past >= 0) {
+                const int32_t* bt = a.block_table + (size_t)job.n * a.max_pages;
+                const int pages = ceil_div(job.past + job.rows / H, P);
+#pragma unroll 4
+                for (int e = lane; e < pages; e += 32) {
                     const int page = __ldg(bt + e);
                     bad |= page < 0 || page >= a.num_pages;
                 }
-                if (bad) misc.bad = 1;
             }
-            float mx = -INFINITY, l = 0.f;  // running maximum (log2 units) and sum
-            bool ok = true;
-            int w = g;
-            for (; w < nitems; w += C::MT) {
-                const int i = w / C::MT, slot = w & 1, tok0 = (t0 + i) * C::KT;
-                const uint32_t s_addr = lanes + slot * C::S_COLS;
-                ok = mbar_wait_warp(&misc.s_full[slot], (w >> 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                uint32_t x[C::KT];
+            bad = __any_sync(0xffffffffu, bad);
+            if (lane == 0) {
+                misc.bad[k & 1] = bad;
+                mbar_arrive(&misc.checked[k & 1]);
+                if (bad && a.status != nullptr) record_error(a.status, MLRA_ERR_DEVICE_BAD_INDEX);
+            }
+            job_done(k);
+        }
+    } else if (C::PAIR && warp == 3) {
+        // ------------------------------------------------------------ pair: room for the other CTA's scores
+        // (a warp of its own: the arrival over there releases what its thread
+        // wrote, and a thread that has just sent scores waits 1000 cycles for that)
+        Job job;
+        int t0, ntiles = 0;
+        bool ok = job_at(0, job);
+        if (ok && job.n >= 0 && job.past >= 0) span(job, t0, ntiles);
+        const int nitems = ntiles * C::MT;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&misc.x_full[0], C::X_BYTES);
+            mbar_arrive_expect_tx(&misc.x_full[1], C::X_BYTES);
+        }
+        for (int w = 0; w + 2 < nitems && ok; ++w) {
+            ok = mbar_wait_warp(&misc.x_read[w & 1], (w >> 1) & 1);
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&misc.x_full[w & 1], C::X_BYTES);
+                mbar_arrive_cluster(map_shared_rank(smem_u32(&misc.x_empty[w & 1]), crank ^ 1));
+            }
+            __syncwarp();
+        }
+        if (!ok && lane == 0) *abort_flag = 1;
+    } else if (C::PAIR && warp >= 8) {
+        // ------------------------------------------------------------ pair: this CTA's share of the scores
+        // each thread sends its row to the same thread of the other CTA, as
+        // [four tokens][row] of 16 bytes, while the softmax is an item behind
+        const int r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t there = map_shared_rank(smem_u32(sm + C::OFF_X) + r * 16, crank ^ 1);
+        const uint32_t full = map_shared_rank(smem_u32(&misc.x_full[0]), crank ^ 1);
+        Job job;
+        int t0, ntiles = 0;
+        bool ok = job_at(0, job);
+        if (ok && job.n >= 0 && job.past >= 0) span(job, t0, ntiles);
+        const int nitems = ntiles * C::MT;
+        for (int w = 0; w < nitems && ok; ++w) {
+            ok = mbar_wait_warp(&misc.s_full[w & 1], (w >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t x[C::KT];
 #pragma unroll
-                for (int c = 0; c < C::KT / 32; ++c) tmem_ld32(s_addr + 32 * c, x + 32 * c);
-                tmem_wait_ld();
-                reg_tie<C::KT>(x);
-                if constexpr (C::PAIR) {
-                    // plus the scores of the other CTA's columns (a sum of two, so both
-                    // CTAs have the same bits)
-                    const float4* here = reinterpret_cast<const float4*>(sm + C::OFF_X + slot * C::X_BYTES) + r;
-                    ok = mbar_wait_warp(&misc.x_full[slot], (w >> 1) & 1);
-                    if (!ok) break;
+            for (int c = 0; c < C::KT / 32; ++c) tmem_ld32(lanes + (w & 1) * C::S_COLS + 32 * c, x + 32 * c);
+            tmem_wait_ld();
+            reg_tie<C::KT>(x);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&misc.x_taken[w & 1]);
+            if (w >= 2) ok = mbar_wait_warp(&misc.x_empty[w & 1], ((w >> 1) - 1) & 1);
+            if (!ok) break;
 #pragma unroll
-                    for (int c = 0; c < C::KT / 4; ++c) {
-                        const float4 v = here[c * 128];
-                        x[4 * c] = __float_as_uint(__uint_as_float(x[4 * c]) + v.x);
-                        x[4 * c + 1] = __float_as_uint(__uint_as_float(x[4 * c + 1]) + v.y);
-                        x[4 * c + 2] = __float_as_uint(__uint_as_float(x[4 * c + 2]) + v.z);
-                        x[4 * c + 3] = __float_as_uint(__uint_as_float(x[4 * c + 3]) + v.w);
+            for (int c = 0; c < C::KT / 4; ++c)
+                st_async_v4(there + (w & 1) * C::X_BYTES + c * 2048, full + (w & 1) * 8, x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+        }
+        if (!ok && lane == 0) *abort_flag = 1;
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ softmax
+        if constexpr (C::MT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        // (a scale of 0 as 1e-30: every finite score still weighs the same, and a
+        // masked score, infinite, stays so)
+        const float sc = a.scale_log2 == 0.f ? 1e-30f : a.scale_log2;
+        const int g = (warp - 4) / 4, quad = warp & 3, r = quad * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+        const uint32_t o_addr = lanes + C::O_COL + g * C::VN;
+        // One loop over the items of all row blocks, a block's end and the next one's
+        // start a branch of it: with a loop over the blocks around it the item loop
+        // came out 9 % slower.
+        // item `at` (of all of this CTA's) covers the tokens from tok0 on
+        uint32_t nth = 0, at = 0, end = 0;
+        int tok0 = 0, pos_first = 0;
+        float mx = 0.f, l = 0.f;  // running maximum (log2 units) and sum
+        bool ok = true, open = false;
+        while (true) {
+            if (at >= end) {
+                if (open) {
+                    const bool some = at != misc.job[nth & 1].tiles * C::MT + g;  // (a part of a split may have no tile)
+                    if (ok && some) {
+                        const uint32_t v = at - C::MT;  // this tile's last item
+                        ok = mbar_wait_warp(&misc.o_done[v & 1], C::MT == 1 ? (v >> 1) & 1 : misc.job[nth & 1].asked & 1);
+                        tc_fence_after();
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&misc.x_read[slot]);
-                    // (P will lie over the scores: they have been taken for sending)
-                    ok = mbar_wait_warp(&misc.x_taken[slot], (w >> 1) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                }
-                // tokens j > limit of the tile are masked (a whole warp's rows at once see it all otherwise)
-                const int limit = pos - tok0;
-                if (pos_first - tok0 < C::KT - 1) {
-                    const uint32_t none = sc < 0.f ? 0x7f800000u : 0xff800000u;
-#pragma unroll
-                    for (int j = 0; j < C::KT; ++j) x[j] = j > limit ? none : x[j];
-                }
-                // the largest scaled score (the smallest raw one under a negative scale)
-                float top[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) top[k] = __uint_as_float(x[k]);
-                if (sc < 0.f) {
-#pragma unroll
-                    for (int j = 4; j < C::KT; ++j) top[j & 3] = fminf(top[j & 3], __uint_as_float(x[j]));
-                    top[0] = fminf(fminf(top[0], top[1]), fminf(top[2], top[3])) * sc;
-                } else {
-#pragma unroll
-                    for (int j = 4; j + 8 <= C::KT; j += 8)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) top[k] = max3(top[k], __uint_as_float(x[j + 2 * k]), __uint_as_float(x[j + 2 * k + 1]));
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], __uint_as_float(x[C::KT - 4 + k]));
-                    top[0] = fmaxf(max3(top[0], top[1], top[2]), top[3]) * sc;
-                }
-                if (i == 0) {
-                    mx = top[0];
-                } else {
-                    const bool grow = top[0] > mx + kRescale;
-                    if (__any_sync(0xffffffffu, grow)) {
-                        // O of this warp's rows at the new maximum, once the PV before is done
-                        if constexpr (C::MT == 1) {
-                            ok = mbar_wait_warp(&misc.o_done[(w - 1) & 1], ((w - 1) >> 1) & 1);
-                            if (!ok) break;
-                            tc_fence_after();
-                        }
-                        const float alpha = grow ? ex2(mx - top[0]) : 1.f;
-                        if (grow) mx = top[0];
-                        l *= alpha;
+                    if (!ok && lane == 0) {
+                        *abort_flag = 1;
+                        if (a.status != nullptr) record_error(a.status, MLRA_ERR_DEVICE_TIMEOUT);
+                    }
+                    const bool bad = !mbar_wait_warp(&misc.checked[nth & 1], (nth >> 1) & 1) || misc.bad[nth & 1] != 0 || !ok;
+                    const Job job = misc.job[nth & 1];  // (again: registers are short in the loop above)
+                    const int row = job.row0 + g * 128 + r, rows = job.rows;
+                    __nv_bfloat16* dst = a.out + (size_t)(job.out0 + row) * W + job.b * DC + rank * C::DL;
+                    if (splits == 1) {
+                        const float inv = a.out_scale / l;
 #pragma unroll 1
                         for (int c = 0; c < C::VN / 32; ++c) {
                             uint32_t o[32];
@@ -613,138 +698,254 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                             tmem_wait_ld();
                             reg_tie<32>(o);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-                            tmem_st32(o_addr + 32 * c, o);
+                            for (int j = 0; j < 32; j += 2)
+                                o[j / 2] = bad ? 0u : pack_bf16(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv);
+                            if (row < rows) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    *reinterpret_cast<uint4*>(dst + 32 * c + 8 * k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                            }
                         }
-                        tmem_wait_st();
+                    } else {
+                        // ---------------------------------------------------- the join of the parts
+                        // Every part's maximum m and sum l of a row, its O scaled to the common
+                        // maximum in shared memory (the operands there are done with), then each
+                        // part sums 1 / splits of the columns over the parts, in their order.
+                        constexpr int ROWS = 128 * C::MT;
+                        float2* stat = reinterpret_cast<float2*>(sm);                 // [row] (m, l)
+                        float4* stage = reinterpret_cast<float4*>(sm + ROWS * 8);     // [four columns][row]
+                        static_assert(ROWS * 8 + ROWS * C::VN * 4 <= C::OFF_MISC, "the stage fits below the barriers");
+                        const int tr = g * 128 + r;
+                        if (!some) mbar_wait_warp(&misc.q_full, 0);  // (else the first scores have)
+                        named_bar_sync<1, 32 * C::SOFT_WARPS>();  // (no MMA of this CTA reads operands any more)
+                        stat[tr] = make_float2(mx, l);
+                        cluster_sync();
+                        float top = -INFINITY, total = 0.f;
+                        for (int p = 0; p < splits; ++p) {
+                            const float2 v = ld_shared_cluster_f2(map_shared_rank(smem_u32(stat + tr), p * C::NV + rank));
+                            const float t = fmaxf(top, v.x);
+                            if (t != -INFINITY) total = total * ex2(top - t) + v.y * ex2(v.x - t);
+                            top = t;
+                        }
+                        const float f = mx != -INFINITY ? ex2(mx - top) : 0.f;
+#pragma unroll 1
+                        for (int c = 0; c < C::VN / 32; ++c) {
+                            uint32_t o[32];
+                            if (some) {
+                                tmem_ld32(o_addr + 32 * c, o);
+                                tmem_wait_ld();
+                                reg_tie<32>(o);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4) {
+                                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                                if (f != 0.f)
+                                    v = make_float4(__uint_as_float(o[j]) * f, __uint_as_float(o[j + 1]) * f, __uint_as_float(o[j + 2]) * f,
+                                                    __uint_as_float(o[j + 3]) * f);
+                                stage[(c * 8 + j / 4) * ROWS + tr] = v;
+                            }
+                        }
+                        cluster_sync();
+                        const float inv = a.out_scale / total;
+                        const int c0 = C::VN / 4 * split >> log_splits, c1 = C::VN / 4 * (split + 1) >> log_splits;  // groups of four columns
+                        for (int c = c0; c < c1; c += 2) {
+                            float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+                            for (int p = 0; p < splits; ++p) {
+                                const uint32_t at = map_shared_rank(smem_u32(stage + c * ROWS + tr), p * C::NV + rank);
+                                const float4 x = ld_shared_cluster_f4(at), y = ld_shared_cluster_f4(at + ROWS * 16);
+                                u.x += x.x, u.y += x.y, u.z += x.z, u.w += x.w;
+                                v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+                            }
+                            uint4 o = make_uint4(pack_bf16(u.x * inv, u.y * inv), pack_bf16(u.z * inv, u.w * inv), pack_bf16(v.x * inv, v.y * inv),
+                                                 pack_bf16(v.z * inv, v.w * inv));
+                            if (bad) o = make_uint4(0u, 0u, 0u, 0u);
+                            if (row < rows) *reinterpret_cast<uint4*>(dst + 4 * c) = o;
+                        }
                     }
+                    tc_fence_before();
+                    job_done(nth++);
+                    if (!ok || C::PAIR) break;
+                    open = false;
                 }
-                // slots behind the last token (stale, or another sequence's) become
-                // zero before the output MMA reads them: 0 * NaN is NaN
-                if (tok0 + C::KT > kv_end) {
-                    uint8_t* tile = sm + C::OFF_C + (i % C::NC) * C::C_BYTES;
-                    const int dead = tok0 + C::KT - kv_end, units = dead * 8;
-                    for (int e = r; e < units * C::NCH; e += 128)
-                        *reinterpret_cast<uint4*>(tile + e / units * C::C_CHUNK + (C::KT - dead) * 128 + e % units * 16) =
-                            make_uint4(0u, 0u, 0u, 0u);
-                    fence_proxy_async_smem();
+                {
+                    Job job;
+                    ok = job_at(nth, job);
+                    if (!ok && lane == 0) *abort_flag = 1;
+                    if (!ok || job.n < 0) break;
+                    const int row = job.row0 + g * 128 + r;
+                    if (job.past < 0) {  // a bad length: zeros
+                        __nv_bfloat16* dst = a.out + (size_t)(job.out0 + row) * W + job.b * DC + rank * C::DL;
+                        for (int c = 0; c < C::VN / 8 && row < job.rows; ++c) *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
+                        job_done(nth++);
+                        continue;
+                    }
+                    int ntiles;
+                    span(job, tok0, ntiles);
+                    tok0 *= C::KT;
+                    at = job.tiles * C::MT + g;
+                    end = (job.tiles + ntiles) * C::MT;
+                    pos_first = job.past + min(row - lane, job.rows - 1) / H;  // last token of the warp's first row
                 }
-                // (a row that has seen no token yet: its scores are all -infinity, and so their
-                // differences stay)
-                const float ref = mx == -INFINITY ? 0.f : mx;
-                const uint64_t sc2 = pack2(sc, sc), mx2 = pack2(-ref, -ref);
-                uint64_t sum[2] = {0, 0};
+                if constexpr (C::QT) {
+                    // this row's latent queries into TMEM (rows past the last: zeros)
+                    const Job job = misc.job[nth & 1];
+                    const size_t y = (size_t)job.out0 + job.row0 + r;
+                    const bool real = y < (size_t)a.tokens * H;
+                    const uint4* src = reinterpret_cast<const uint4*>(a.q_lat + y * W + job.b * DC + rank * C::DL);
 #pragma unroll
-                for (int j = 0; j < C::KT; j += 2) {
-                    float p0, p1;
-                    unpack2(fma2(pack2(x[j], x[j + 1]), sc2, mx2), p0, p1);
-                    p0 = ex2(p0);
-                    p1 = ex2(p1);
-                    sum[j / 2 & 1] = add2(sum[j / 2 & 1], pack2(p0, p1));
-                    x[j / 2] = pack_bf16(p0, p1);
-                }
+                    for (int c = 0; c < C::NCH; ++c) {
+                        uint32_t q[32];
 #pragma unroll
-                for (int c = 0; c < C::KT / 64; ++c) tmem_st32(s_addr + 32 * c, x + 32 * c);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&misc.p_full[slot]);
-                float s0, s1;
-                unpack2(add2(sum[0], sum[1]), s0, s1);
-                l += s0 + s1;
+                        for (int u = 0; u < 8; ++u) {
+                            const uint4 v = real ? __ldg(src + 8 * c + u) : make_uint4(0u, 0u, 0u, 0u);
+                            q[4 * u] = v.x, q[4 * u + 1] = v.y, q[4 * u + 2] = v.z, q[4 * u + 3] = v.w;
+                        }
+                        tmem_st32(lanes + C::Q_COL + 32 * c, q);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&misc.q_tmem);
+                }
+                mx = -INFINITY, l = 0.f;
+                open = true;
+                if (at >= end) continue;
             }
-            if (ok && nitems > 0) {
-                const int v = w - C::MT;  // this tile's last item
-                ok = mbar_wait_warp(&misc.o_done[v & 1], C::MT == 1 ? (v >> 1) & 1 : 0);
+            const uint32_t slot = at & 1, parity = (at >> 1) & 1;
+            const uint32_t s_addr = lanes + slot * C::S_COLS;
+            ok = mbar_wait_warp(&misc.s_full[slot], parity);
+            if (!ok) {
+                at = end;
+                continue;
+            }
+            tc_fence_after();
+            uint32_t x[C::KT];
+#pragma unroll
+            for (int c = 0; c < C::KT / 32; ++c) tmem_ld32(s_addr + 32 * c, x + 32 * c);
+            tmem_wait_ld();
+            reg_tie<C::KT>(x);
+            if constexpr (C::PAIR) {
+                // plus the scores of the other CTA's columns (a sum of two, so both
+                // CTAs have the same bits)
+                const float4* here = reinterpret_cast<const float4*>(sm + C::OFF_X + slot * C::X_BYTES) + r;
+                ok = mbar_wait_warp(&misc.x_full[slot], parity);
+                if (!ok) {
+                at = end;
+                continue;
+            }
+#pragma unroll
+                for (int c = 0; c < C::KT / 4; ++c) {
+                    const float4 v = here[c * 128];
+                    x[4 * c] = __float_as_uint(__uint_as_float(x[4 * c]) + v.x);
+                    x[4 * c + 1] = __float_as_uint(__uint_as_float(x[4 * c + 1]) + v.y);
+                    x[4 * c + 2] = __float_as_uint(__uint_as_float(x[4 * c + 2]) + v.z);
+                    x[4 * c + 3] = __float_as_uint(__uint_as_float(x[4 * c + 3]) + v.w);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&misc.x_read[slot]);
+                // (P will lie over the scores: they have been taken for sending)
+                ok = mbar_wait_warp(&misc.x_taken[slot], parity);
+                if (!ok) {
+                at = end;
+                continue;
+            }
                 tc_fence_after();
             }
-            if (!ok && lane == 0) {
-                *abort_flag = 1;
-                if (a.status != nullptr) record_error(a.status, MLRA_ERR_DEVICE_TIMEOUT);
+            // tokens j > limit of the tile are masked (a whole warp's rows at once see it all otherwise)
+            if (pos_first - tok0 < C::KT - 1) {
+                const Job& job = misc.job[nth & 1];
+                const int limit = job.past + min(job.row0 + g * 128 + r, job.rows - 1) / H - tok0;  // of this row
+                const uint32_t none = sc < 0.f ? 0x7f800000u : 0xff800000u;
+#pragma unroll
+                for (int j = 0; j < C::KT; ++j) x[j] = j > limit ? none : x[j];
             }
-            named_bar_sync<1, 32 * C::SOFT_WARPS>();  // every page check is in
-            const bool bad = misc.bad != 0 || !ok;
-            if (misc.bad != 0 && threadIdx.x == 128 && a.status != nullptr) record_error(a.status, MLRA_ERR_DEVICE_BAD_INDEX);
-            __nv_bfloat16* dst = a.out + (out0 + g * 128 + r) * W + col0;
-            if (splits == 1) {
-                const float inv = a.out_scale / l;
-#pragma unroll 1
-                for (int c = 0; c < C::VN / 32; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32(o_addr + 32 * c, o);
-                    tmem_wait_ld();
-                    reg_tie<32>(o);
+            // the largest scaled score (the smallest raw one under a negative scale)
+            float top[4];
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2)
-                        o[j / 2] = bad ? 0u : pack_bf16(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv);
-                    if (row < rows) {
+            for (int k = 0; k < 4; ++k) top[k] = __uint_as_float(x[k]);
+            if (sc < 0.f) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            *reinterpret_cast<uint4*>(dst + 32 * c + 8 * k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                    }
-                }
+                for (int j = 4; j < C::KT; ++j) top[j & 3] = fminf(top[j & 3], __uint_as_float(x[j]));
+                top[0] = fminf(fminf(top[0], top[1]), fminf(top[2], top[3])) * sc;
             } else {
-                // ---------------------------------------------------- the join of the parts
-                // Every part's maximum m and sum l of a row, its O scaled to the common
-                // maximum in shared memory (the operands there are done with), then each
-                // part sums 1 / splits of the columns over the parts, in their order.
-                constexpr int ROWS = 128 * C::MT;
-                float2* stat = reinterpret_cast<float2*>(sm);                 // [row] (m, l)
-                float4* stage = reinterpret_cast<float4*>(sm + ROWS * 8);     // [four columns][row]
-                static_assert(ROWS * 8 + ROWS * C::VN * 4 <= C::OFF_MISC, "the stage fits below the barriers");
-                const int tr = g * 128 + r;
-                if (nitems == 0) mbar_wait_warp(&misc.q_full, 0);  // (else the first scores have)
-                named_bar_sync<1, 32 * C::SOFT_WARPS>();  // (no MMA of this CTA reads operands any more)
-                stat[tr] = make_float2(nitems > 0 ? mx : -INFINITY, l);
-                cluster_sync();
-                float top = -INFINITY, total = 0.f;
-                for (int p = 0; p < splits; ++p) {
-                    const float2 v = ld_shared_cluster_f2(map_shared_rank(smem_u32(stat + tr), p * C::NV + rank));
-                    const float t = fmaxf(top, v.x);
-                    if (t != -INFINITY) total = total * ex2(top - t) + v.y * ex2(v.x - t);
-                    top = t;
-                }
-                const float f = nitems > 0 && mx != -INFINITY ? ex2(mx - top) : 0.f;
-#pragma unroll 1
-                for (int c = 0; c < C::VN / 32; ++c) {
-                    uint32_t o[32];
-                    if (f != 0.f || nitems > 0) {
-                        tmem_ld32(o_addr + 32 * c, o);
-                        tmem_wait_ld();
-                        reg_tie<32>(o);
-                    }
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (f != 0.f)
-                            v = make_float4(__uint_as_float(o[j]) * f, __uint_as_float(o[j + 1]) * f, __uint_as_float(o[j + 2]) * f,
-                                            __uint_as_float(o[j + 3]) * f);
-                        stage[(c * 8 + j / 4) * ROWS + tr] = v;
+                for (int j = 4; j + 8 <= C::KT; j += 8)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) top[k] = max3(top[k], __uint_as_float(x[j + 2 * k]), __uint_as_float(x[j + 2 * k + 1]));
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], __uint_as_float(x[C::KT - 4 + k]));
+                top[0] = fmaxf(max3(top[0], top[1], top[2]), top[3]) * sc;
+            }
+            {
+                // (a row that has seen no token yet: its O, not begun or of zero weights, stays)
+                const bool none = mx == -INFINITY;
+                const bool grow = !none && top[0] > mx + kRescale;
+                if (none) mx = top[0];
+                if (__any_sync(0xffffffffu, grow)) {
+                    // O of this warp's rows at the new maximum, once the PV before is done
+                    if constexpr (C::MT == 1) {
+                        ok = mbar_wait_warp(&misc.o_done[(at - 1) & 1], ((at - 1) >> 1) & 1);
+                        if (!ok) {
+                at = end;
+                continue;
+            }
+                        tc_fence_after();
                     }
-                }
-                cluster_sync();
-                const float inv = a.out_scale / total;
-                const int c0 = C::VN / 4 * split >> log_splits, c1 = C::VN / 4 * (split + 1) >> log_splits;  // groups of four columns
-                for (int c = c0; c < c1; c += 2) {
-                    float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
-                    for (int p = 0; p < splits; ++p) {
-                        const uint32_t at = map_shared_rank(smem_u32(stage + c * ROWS + tr), p * C::NV + rank);
-                        const float4 x = ld_shared_cluster_f4(at), y = ld_shared_cluster_f4(at + ROWS * 16);
-                        u.x += x.x, u.y += x.y, u.z += x.z, u.w += x.w;
-                        v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+                    const float alpha = grow ? ex2(mx - top[0]) : 1.f;
+                    if (grow) mx = top[0];
+                    l *= alpha;
+#pragma unroll 1
+                    for (int c = 0; c < C::VN / 16; ++c) {
+                        float o[16];
+                        tmem_ld16(o_addr + 16 * c, o);
+                        tmem_wait_ld(o);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] *= alpha;
+                        tmem_st16(o_addr + 16 * c, o);
                     }
-                    uint4 o = make_uint4(pack_bf16(u.x * inv, u.y * inv), pack_bf16(u.z * inv, u.w * inv), pack_bf16(v.x * inv, v.y * inv),
-                                         pack_bf16(v.z * inv, v.w * inv));
-                    if (bad) o = make_uint4(0u, 0u, 0u, 0u);
-                    if (row < rows) *reinterpret_cast<uint4*>(dst + 4 * c) = o;
+                    tmem_wait_st();
                 }
             }
+            // slots behind the last token (stale, or another sequence's) become
+            // zero before the output MMA reads them: 0 * NaN is NaN
+            if (at + C::MT >= end && tok0 + C::KT > misc.job[nth & 1].kv_end) {
+                uint8_t* tile = sm + C::OFF_C + (at / C::MT % C::NC) * C::C_BYTES;
+                const int dead = tok0 + C::KT - misc.job[nth & 1].kv_end, units = dead * 8;
+                for (int e = r; e < units * C::NCH; e += 128)
+                    *reinterpret_cast<uint4*>(tile + e / units * C::C_CHUNK + (C::KT - dead) * 128 + e % units * 16) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+            }
+            // (a row that has seen no token yet: its scores are all -infinity, and so their
+            // differences stay)
+            const float ref = mx == -INFINITY ? 0.f : mx;
+            const uint64_t sc2 = pack2(sc, sc), mx2 = pack2(-ref, -ref);
+            uint64_t sum[2] = {0, 0};
+#pragma unroll
+            for (int j = 0; j < C::KT; j += 2) {
+                float p0, p1;
+                unpack2(fma2(pack2(x[j], x[j + 1]), sc2, mx2), p0, p1);
+                p0 = ex2(p0);
+                p1 = ex2(p1);
+                sum[j / 2 & 1] = add2(sum[j / 2 & 1], pack2(p0, p1));
+                x[j / 2] = pack_bf16(p0, p1);
+            }
+#pragma unroll
+            for (int c = 0; c < C::KT / 64; ++c) tmem_st32(s_addr + 32 * c, x + 32 * c);
+            tmem_wait_st();
             tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&misc.p_full[slot]);
+            float s0, s1;
+            unpack2(add2(sum[0], sum[1]), s0, s1);
+            l += s0 + s1;
+            at += C::MT;
+            tok0 += C::KT;
         }
-        if (splits > 1 && (warp < 4 || warp >= 4 + C::SOFT_WARPS)) {  // the softmax warps' meetings in the join
-            cluster_sync();
-            cluster_sync();
-        }
+    }
+    if (splits > 1 && misc.job[0].n >= 0 && misc.job[0].past >= 0 && (warp < 4 || warp >= 4 + C::SOFT_WARPS)) {  // the softmax warps' meetings in the join
+        cluster_sync();
+        cluster_sync();
     }
     __syncwarp();
     if (cluster > 1) cluster_sync();  // (no other CTA reads or writes this one's memory any more)

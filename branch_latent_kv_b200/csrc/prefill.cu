@@ -158,13 +158,15 @@ struct Misc {
     uint64_t q_full, q_empty;  // the queries in shared memory; every score MMA of the row block has read them
     // row block k of this CTA in place k % 2: it is known; its pages are checked; every reader is done with it
     uint64_t job_full[2], checked[2], job_empty[2];
-    uint64_t next_full;
+    // answers to requests for another CTA's place are here; a pair, whose second CTA
+    // hears them from the first: they have been read there
+    uint64_t next_full[2], next_read[2];
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
     int bad[2];  // a page of the sequence lies outside the pool
     Job job[2];
-    alignas(16) uint32_t next[4];  // the answer to a request for another CTA's place
+    alignas(16) uint32_t next[2][4];
 };
 
 struct Maps {
@@ -360,9 +362,9 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
         for (int i = 0; i < 2; ++i) {
             mbar_init(&misc.job_full[i], 1);
             mbar_init(&misc.checked[i], 1);
-            mbar_init(&misc.job_empty[i], 2 + C::SOFT_WARPS);  // the MMA warp, the page check, the softmax warps
+            mbar_init(&misc.job_empty[i], 2 + C::SOFT_WARPS + (C::PAIR ? 5 : 0));  // the warps that read it
         }
-        mbar_init(&misc.next_full, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&misc.next_full[i], 1), mbar_init(&misc.next_read[i], 1);
         mbar_init(&misc.drain, 1);
         misc.abort_flag = 0;
         misc.job[0].n = -1;
@@ -442,20 +444,33 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                 }
                 __syncwarp();
             }
-            if (!ok || C::PAIR || cluster > 1) break;
-            // the place of a CTA that has not started, asked for when this row block's
-            // last copy is under way
-            if (lane == 0) {
-                fence_proxy_async_smem();  // (the answer before this one has been read)
-                mbar_arrive_expect_tx(&misc.next_full, 16);
-                request_place(misc.next, &misc.next_full);
-            }
-            ok = mbar_wait_warp(&misc.next_full, requests++ & 1);
+            if (!ok || log_splits > 0) break;
+            // the place of a CTA (or pair) that has not started, asked for when this row
+            // block's last copy is under way
+            const uint32_t at = requests & 1, phase = (requests >> 1) & 1;
+            if (C::PAIR && rank == 0 && requests >= 2) ok = mbar_wait_warp(&misc.next_read[at], phase ^ 1);
             if (!ok) break;
-            const int next = place_taken(misc.next);
+            ++requests;
+            if (lane == 0) {
+                fence_proxy_async_smem();  // (the answer that was here has been read)
+                mbar_arrive_expect_tx(&misc.next_full[at], 16);
+                if (rank == 0) request_place(misc.next[at], &misc.next_full[at]);
+            }
+            ok = mbar_wait_warp(&misc.next_full[at], phase);
+            if (!ok) break;
+            int next;
+            if (rank == 0) {
+                next = place_taken(misc.next[at]);
+                if (C::PAIR && lane == 0)
+                    st_async_v4(map_shared_rank(smem_u32(misc.next[at]), 1), map_shared_rank(smem_u32(&misc.next_full[at]), 1), (uint32_t)next, 0u, 0u, 0u);
+            } else {
+                next = (int)*reinterpret_cast<volatile uint32_t*>(misc.next[at]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_shared_rank(smem_u32(&misc.next_read[at]), 0));
+            }
             __syncwarp();
             if (next < 0) break;
-            id = next;
+            id = next / C::NV;
             if (blocks >= 2) ok = mbar_wait_warp(&misc.job_empty[blocks & 1], ((blocks >> 1) - 1) & 1);
             if (!ok) break;
             have = take(id, blocks, done, asked);
@@ -471,7 +486,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             // no copy or answer may land after this CTA has gone
             constexpr uint64_t kLong = 200000000ull;
             if (asked > 0 && ok0) mbar_wait(&misc.q_full, (asked - 1) & 1, kLong);
-            if (requests > 0) mbar_wait(&misc.next_full, (requests - 1) & 1, kLong);
+            if (requests > 0) mbar_wait(&misc.next_full[(requests - 1) & 1], ((requests - 1) >> 1) & 1, kLong);
             for (uint32_t i = done > C::NK ? done - C::NK : 0; i < done; ++i) mbar_wait(&misc.k_full[i % C::NK], (i / C::NK) & 1, kLong);
             for (uint32_t i = done > C::NC ? done - C::NC : 0; i < done; ++i) mbar_wait(&misc.c_full[i % C::NC], (i / C::NC) & 1, kLong);
         }
@@ -568,7 +583,6 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                 if (more) c_new.next(C::NC), k_new.next(C::NK);
                 if ((i & 7) == 7 && __shfl_sync(0xffffffffu, *abort_flag, 0)) ok = false;
             }
-            if (C::PAIR) break;
         }
         if (!ok && lane == 0) *abort_flag = 1;
         // every MMA has finished before TMEM is freed
@@ -604,23 +618,27 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
         // ------------------------------------------------------------ pair: room for the other CTA's scores
         // (a warp of its own: the arrival over there releases what its thread
         // wrote, and a thread that has just sent scores waits 1000 cycles for that)
-        Job job;
-        int t0, ntiles = 0;
-        bool ok = job_at(0, job);
-        if (ok && job.n >= 0 && job.past >= 0) span(job, t0, ntiles);
-        const int nitems = ntiles * C::MT;
+        bool ok = true;
         if (lane == 0) {
             mbar_arrive_expect_tx(&misc.x_full[0], C::X_BYTES);
             mbar_arrive_expect_tx(&misc.x_full[1], C::X_BYTES);
         }
-        for (int w = 0; w + 2 < nitems && ok; ++w) {
-            ok = mbar_wait_warp(&misc.x_read[w & 1], (w >> 1) & 1);
-            if (!ok) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&misc.x_full[w & 1], C::X_BYTES);
-                mbar_arrive_cluster(map_shared_rank(smem_u32(&misc.x_empty[w & 1]), crank ^ 1));
+        for (uint32_t k = 0; ok; ++k) {
+            Job job;
+            ok = job_at(k, job);
+            if (!ok || job.n < 0) break;
+            int t0, ntiles = 0;
+            if (job.past >= 0) span(job, t0, ntiles);
+            for (uint32_t at = job.tiles; at < job.tiles + ntiles && ok; ++at) {
+                ok = mbar_wait_warp(&misc.x_read[at & 1], (at >> 1) & 1);
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&misc.x_full[at & 1], C::X_BYTES);
+                    mbar_arrive_cluster(map_shared_rank(smem_u32(&misc.x_empty[at & 1]), crank ^ 1));
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            job_done(k);
         }
         if (!ok && lane == 0) *abort_flag = 1;
     } else if (C::PAIR && warp >= 8) {
@@ -631,28 +649,34 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t there = map_shared_rank(smem_u32(sm + C::OFF_X) + r * 16, crank ^ 1);
         const uint32_t full = map_shared_rank(smem_u32(&misc.x_full[0]), crank ^ 1);
-        Job job;
-        int t0, ntiles = 0;
-        bool ok = job_at(0, job);
-        if (ok && job.n >= 0 && job.past >= 0) span(job, t0, ntiles);
-        const int nitems = ntiles * C::MT;
-        for (int w = 0; w < nitems && ok; ++w) {
-            ok = mbar_wait_warp(&misc.s_full[w & 1], (w >> 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            uint32_t x[C::KT];
+        bool ok = true;
+        for (uint32_t k = 0; ok; ++k) {
+            Job job;
+            ok = job_at(k, job);
+            if (!ok || job.n < 0) break;
+            int t0, ntiles = 0;
+            if (job.past >= 0) span(job, t0, ntiles);
+            const uint32_t end = job.tiles + ntiles;
+            for (uint32_t at = job.tiles; at < end && ok; ++at) {
+                const uint32_t slot = at & 1;
+                ok = mbar_wait_warp(&misc.s_full[slot], (at >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t x[C::KT];
 #pragma unroll
-            for (int c = 0; c < C::KT / 32; ++c) tmem_ld32(lanes + (w & 1) * C::S_COLS + 32 * c, x + 32 * c);
-            tmem_wait_ld();
-            reg_tie<C::KT>(x);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&misc.x_taken[w & 1]);
-            if (w >= 2) ok = mbar_wait_warp(&misc.x_empty[w & 1], ((w >> 1) - 1) & 1);
-            if (!ok) break;
+                for (int c = 0; c < C::KT / 32; ++c) tmem_ld32(lanes + slot * C::S_COLS + 32 * c, x + 32 * c);
+                tmem_wait_ld();
+                reg_tie<C::KT>(x);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&misc.x_taken[slot]);
+                if (at >= 2) ok = mbar_wait_warp(&misc.x_empty[slot], ((at >> 1) - 1) & 1);
+                if (!ok) break;
 #pragma unroll
-            for (int c = 0; c < C::KT / 4; ++c)
-                st_async_v4(there + (w & 1) * C::X_BYTES + c * 2048, full + (w & 1) * 8, x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+                for (int c = 0; c < C::KT / 4; ++c)
+                    st_async_v4(there + slot * C::X_BYTES + c * 2048, full + slot * 8, x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+            }
+            job_done(k);
         }
         if (!ok && lane == 0) *abort_flag = 1;
     } else if (warp >= 4) {
@@ -764,7 +788,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                     }
                     tc_fence_before();
                     job_done(nth++);
-                    if (!ok || C::PAIR) break;
+                    if (!ok) break;
                     open = false;
                 }
                 {

@@ -5,6 +5,9 @@ graphs, and the path prompt -> pre-step -> prompt attention -> decode.
 
 The probabilities enter the output product as bf16 (half a step: 2^-8)."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -228,6 +231,79 @@ def test_bad_sequences_are_reported_and_zeroed():
         assert int(status.item()) == b.MLRA_ERR_DEVICE_BAD_SEQLEN, cu
     b.mlra_prefill(**_gpu(c), device_status=status)
     assert int(status.item()) == 0  # each call reports its own
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("branches,d_c,heads", [(4, 64, 16), (1, 128, 40), (4, 128, 16), (2, 256, 16), (1, 512, 16)])
+def test_more_row_blocks_than_the_gpu_holds(branches, d_c, heads):
+    """Several row blocks one after the other on each SM, of any length, empty
+    sequences and bad ones among them."""
+    rng = np.random.default_rng(40)
+    new = [int(q) for q in rng.integers(0, 41, 150)] + [500, 1, 333]
+    past = [int(p) for p in rng.integers(1, 260, len(new))]
+    c = _case(41, heads, branches, d_c, 64, 32, new, past)
+    short, torn = (n for n in (20, 90) if new[n] > 0)
+    want, tol = _expect(c)
+    for n in (short, torn):
+        lo, hi = int(c["cu_seqlens"][n]), int(c["cu_seqlens"][n + 1])
+        want[lo:hi], tol[lo:hi] = 0, 0
+    c["seqlens"][short] = new[short] - 1
+    c["block_table"][torn, 0] = -1
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = b.mlra_prefill(**_gpu(c), out=torch.full_like(c["q_lat"], 3.0).cuda(), device_status=status)
+    assert int(status.item()) in (b.MLRA_ERR_DEVICE_BAD_SEQLEN, b.MLRA_ERR_DEVICE_BAD_INDEX)
+    ref.within(got, want, tol)
+    again = b.mlra_prefill(**_gpu(c))
+    assert torch.equal(again, got)
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once():
+    """Calls on two streams that share the GPU's SMs: the results of each alone."""
+    one = _gpu(_case(42, 16, 4, 128, 64, 64, [700, 300], [0, 200]))
+    two = _gpu(_case(43, 16, 4, 64, 32, 32, [600, 90, 400], [10, 0, 77]))
+    want = [b.mlra_prefill(**one), b.mlra_prefill(**two)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[torch.empty_like(w) for _ in range(4)] for w in want]
+    torch.cuda.synchronize()
+    for i in range(4):
+        for c, s, o in zip((one, two), streams, outs):
+            b.mlra_prefill(**c, out=o[i], stream=s)
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(w, x) for x in o)
+
+
+FIRST_CALL = """
+import torch
+from branch_latent_kv_b200 import binding as b
+torch.manual_seed(0)
+new = lambda *s: torch.randn(*s, device="cuda").to(torch.bfloat16)
+i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+q, qr, lat, rope = new(70, 8, 2, 128), new(70, 8, 64), new(3, 64, 2, 128), new(3, 64, 64)
+lat8, sig = torch.zeros(3, 64, 2, 128, device="cuda", dtype=torch.float8_e4m3fn), torch.ones(3, 4, 2, device="cuda")
+table, lens, cu = i32(2, 0).view(1, 2), i32(70), i32(0, 70)
+graph = torch.cuda.CUDAGraph()
+def calls():
+    x = b.mlra_prefill(q, qr, lat, rope, table, lens, cu, 0.1, 1.0)
+    b.mlra_append_fp8(lat[:1].view(64, 2, 128)[:6], rope[0, :6], i6, lens, table, lat8, sig, rope8)
+    return x, b.mlra_decode_fp8(q[:1], qr[:1], lat8, sig, rope8, table, lens, 0.1, 1.0)
+i6, rope8 = i32(0, 6), torch.zeros(3, 64, 64, device="cuda", dtype=torch.bfloat16)
+with torch.cuda.graph(graph):
+    got = calls()
+graph.replay()
+want = calls()
+assert all(torch.equal(x, y) for x, y in zip(got, want)) and bool(got[0].isfinite().all())
+print("the same")
+"""
+
+
+@pytest.mark.gpu
+def test_first_calls_of_a_process_are_captured():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "the same" in run.stdout, run.stderr[-2000:]
 
 
 @pytest.mark.gpu

@@ -35,7 +35,8 @@
 // takes the place of one that has not started (cluster launch control): the
 // next block's queries, first tiles and first scores come while this one's
 // last softmax and its output are under way.  Prompts of 1 to 1024 tokens, 612
-// blocks: 54 us against 67 with a new CTA for every block.
+// blocks: 54 us against 67 with a new CTA for every block.  (Where a block's
+// tokens are split, all blocks run at once and each CTA has one.)
 //
 // What the widths ask for, with what it measured:
 //  - d_c <= 128: tiles of 128 x 128 scores, a row of them in one thread's
@@ -49,7 +50,8 @@
 //    other (st.async to its shared memory), the softmax adds the two.  Two
 //    prompts of 3937 tokens together, 16 heads: 603 us with all scores computed
 //    twice, 319 as a pair, 252 with the queries in TMEM and the scores sent by
-//    warps of their own (8 to 11).
+//    warps of their own (8 to 11), 241 with blocks one after the other, 234 with
+//    the next block's queries written before this one's output.
 //  - few row blocks: a cluster of up to 8 CTAs divides a block's tokens, and
 //    joins outputs, maxima and sums over distributed shared memory (one new
 //    token after 8191 of four 128-wide branches: 28 us against 129).
@@ -689,13 +691,33 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t o_addr = lanes + C::O_COL + g * C::VN;
         // One loop over the items of all row blocks, a block's end and the next one's
-        // start a branch of it: with a loop over the blocks around it the item loop
-        // came out 9 % slower.
-        // item `at` (of all of this CTA's) covers the tokens from tok0 on
+        // start a branch of it (8192 tokens 1076 us; with a loop over the blocks
+        // around a loop over their items 1120).  Item `at`, of all of this CTA's,
+        // covers the tokens from tok0 on.
         uint32_t nth = 0, at = 0, end = 0;
         int tok0 = 0, pos_first = 0;
         float mx = 0.f, l = 0.f;  // running maximum (log2 units) and sum
-        bool ok = true, open = false;
+        bool ok = true, open = false, asked = false;
+        // QT: this row's latent queries of a row block into TMEM (rows past the last: zeros)
+        auto put_queries = [&](const Job& job) {
+            const size_t y = (size_t)job.out0 + job.row0 + r;
+            const bool real = y < (size_t)a.tokens * H;
+            const uint4* src = reinterpret_cast<const uint4*>(a.q_lat + y * W + job.b * DC + rank * C::DL);
+#pragma unroll
+            for (int c = 0; c < C::NCH; ++c) {
+                uint32_t q[32];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const uint4 v = real ? __ldg(src + 8 * c + u) : make_uint4(0u, 0u, 0u, 0u);
+                    q[4 * u] = v.x, q[4 * u + 1] = v.y, q[4 * u + 2] = v.z, q[4 * u + 3] = v.w;
+                }
+                tmem_st32(lanes + C::Q_COL + 32 * c, q);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&misc.q_tmem);
+        };
         while (true) {
             if (at >= end) {
                 if (open) {
@@ -704,6 +726,12 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                         const uint32_t v = at - C::MT;  // this tile's last item
                         ok = mbar_wait_warp(&misc.o_done[v & 1], C::MT == 1 ? (v >> 1) & 1 : misc.job[nth & 1].asked & 1);
                         tc_fence_after();
+                    }
+                    if constexpr (C::QT) {
+                        // the next block's queries before this one's output: no MMA reads the old ones any more
+                        Job next;
+                        asked = ok && splits == 1 && job_at(nth + 1, next) && next.n >= 0 && next.past >= 0;
+                        if (asked) put_queries(next);
                     }
                     if (!ok && lane == 0) {
                         *abort_flag = 1;
@@ -811,25 +839,8 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                     pos_first = job.past + min(row - lane, job.rows - 1) / H;  // last token of the warp's first row
                 }
                 if constexpr (C::QT) {
-                    // this row's latent queries into TMEM (rows past the last: zeros)
-                    const Job job = misc.job[nth & 1];
-                    const size_t y = (size_t)job.out0 + job.row0 + r;
-                    const bool real = y < (size_t)a.tokens * H;
-                    const uint4* src = reinterpret_cast<const uint4*>(a.q_lat + y * W + job.b * DC + rank * C::DL);
-#pragma unroll
-                    for (int c = 0; c < C::NCH; ++c) {
-                        uint32_t q[32];
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            const uint4 v = real ? __ldg(src + 8 * c + u) : make_uint4(0u, 0u, 0u, 0u);
-                            q[4 * u] = v.x, q[4 * u + 1] = v.y, q[4 * u + 2] = v.z, q[4 * u + 3] = v.w;
-                        }
-                        tmem_st32(lanes + C::Q_COL + 32 * c, q);
-                    }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&misc.q_tmem);
+                    if (!asked) put_queries(misc.job[nth & 1]);
+                    asked = false;
                 }
                 mx = -INFINITY, l = 0.f;
                 open = true;

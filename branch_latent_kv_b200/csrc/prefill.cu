@@ -35,7 +35,7 @@
 // takes the place of one that has not started (cluster launch control): the
 // next block's queries, first tiles and first scores come while this one's
 // last softmax and its output are under way.  Prompts of 1 to 1024 tokens, 612
-// blocks: 54 us against 67 with a new CTA for every block.  (Where a block's
+// blocks: 49 us, where a new CTA for every block cost 12 us more.  (Where a block's
 // tokens are split, all blocks run at once and each CTA has one.)
 //
 // What the widths ask for, with what it measured:
@@ -215,6 +215,24 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// One step of a 4 x 4 transpose of 16-byte pieces o[4 k ..] between the lanes of
+// a group of four: lanes BIT apart exchange the pieces whose index differs in BIT.
+template <int BIT>
+__device__ __forceinline__ void swap_quarters(uint32_t* o, int lane) {
+    const bool hi = lane & BIT;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (k & BIT) continue;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            uint32_t &x = o[4 * k + u], &y = o[4 * (k | BIT) + u];
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? x : y, BIT);
+            if (hi) x = got;
+            else y = got;
+        }
+    }
 }
 
 // Row blocks ("places") of sequence n, whose offset is c0, start at c0 H / BM +
@@ -752,7 +770,20 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
 #pragma unroll
                             for (int j = 0; j < 32; j += 2)
                                 o[j / 2] = bad ? 0u : pack_bf16(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv);
-                            if (row < rows) {
+                            if constexpr (C::MT == 2) {
+                                // lane i of four takes the i-th 16 bytes of each of their rows: a store
+                                // covers 64 bytes of eight rows, not 16 of 32 (packed prompts 49 us against
+                                // 54; with one warp on a scheduler the exchange costs more: d_c = 512 240
+                                // against 234)
+                                swap_quarters<1>(o, lane);
+                                swap_quarters<2>(o, lane);
+                                const int i = lane & 3;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    if (row - i + k < rows)
+                                        *reinterpret_cast<uint4*>(dst + (long long)(k - i) * (long long)W + 32 * c + 8 * i) =
+                                            make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                            } else if (row < rows) {
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
                                     *reinterpret_cast<uint4*>(dst + 32 * c + 8 * k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);

@@ -458,11 +458,13 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                 }
             }
             if (id == 0 && a.status != nullptr) {  // offsets out of range, whichever places they claim
+                bool bad = false;
+#pragma unroll 4
                 for (int m = lane; m < a.batch; m += 32) {
                     const int c0 = __ldg(a.cu_seqlens + m), c1 = __ldg(a.cu_seqlens + m + 1);
-                    if (c0 < 0 || c1 < c0 || c1 > a.tokens) record_error(a.status, MLRA_ERR_DEVICE_BAD_SEQLEN);
+                    bad |= c0 < 0 || c1 < c0 || c1 > a.tokens;
                 }
-                __syncwarp();
+                if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(a.status, MLRA_ERR_DEVICE_BAD_SEQLEN);
             }
             if (!ok || log_splits > 0) break;
             // the place of a CTA (or pair) that has not started, asked for when this row

@@ -324,6 +324,23 @@ def test_length_one_is_the_latent():
 
 
 @pytest.mark.gpu
+def test_a_query_that_is_not_finite_stays_in_its_head():
+    c = _decode_case(33, 20, 4, 128, 64, 64, [700, 5000, 30])
+    out, tol = _expect(c)
+    c["q_lat"][0, 3, 1, 5] = float("nan")
+    c["q_lat"][1, 18, 0, 127] = float("inf")
+    c["q_lat"][1, 2, 3, 0] = -float("inf")
+    c["q_rope"][2, 7, 9] = float("nan")
+    got = b.mlra_decode_fp8(**_gpu(c)).double().cpu()
+    lost = torch.zeros(got.shape[:3], dtype=torch.bool)
+    for at in ((0, 3, 1), (1, 18, 0), (1, 2, 3)):
+        lost[at] = True
+    lost[2, 7] = True
+    assert bool(got[lost].isnan().all())
+    ref.within(got[~lost], out[~lost], tol[~lost])
+
+
+@pytest.mark.gpu
 def test_page_order_and_repeats_give_the_same_bits():
     c = _decode_case(28, 16, 4, 128, 64, 64, [3000, 1, 640, 129, 2049])
     perm = torch.randperm(c["latent_cache"].shape[0], generator=torch.Generator().manual_seed(2))

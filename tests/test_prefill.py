@@ -197,6 +197,23 @@ def test_page_order_and_company_do_not_change_a_sequence():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("branches,d_c", [(4, 128), (2, 256), (1, 512)])
+def test_a_query_that_is_not_finite_stays_in_its_row(branches, d_c):
+    c = _case(24, 8, branches, d_c, 64, 64, [70, 33], [100, 0])
+    out, tol = _expect(c)
+    last = branches - 1
+    c["q_lat"][5, 3, last, 7] = float("nan")
+    c["q_lat"][69, 0, 0, d_c - 1] = float("inf")
+    c["q_rope"][71, 7, 1] = float("nan")
+    got = b.mlra_prefill(**_gpu(c)).double().cpu()
+    lost = torch.zeros(got.shape[:3], dtype=torch.bool)
+    lost[5, 3, last] = lost[69, 0, 0] = True
+    lost[71, 7] = True
+    assert bool(got[lost].isnan().all())
+    ref.within(got[~lost], out[~lost], tol[~lost])
+
+
+@pytest.mark.gpu
 def test_rows_of_no_sequence_stay():
     c = _case(9, 16, 2, 128, 64, 64, [50, 20], [0, 0])
     T = 70

@@ -468,7 +468,8 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             }
             if (!ok || log_splits > 0) break;
             // the place of a CTA (or pair) that has not started, asked for when this row
-            // block's last copy is under way
+            // block's last copy is under way (packed prompts 48.9 us; four tiles earlier
+            // 51.4: the CTAs end further apart)
             const uint32_t at = requests & 1, phase = (requests >> 1) & 1;
             if (C::PAIR && rank == 0 && requests >= 2) ok = mbar_wait_warp(&misc.next_read[at], phase ^ 1);
             if (!ok) break;

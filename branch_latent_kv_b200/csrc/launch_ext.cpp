@@ -34,6 +34,24 @@ decltype(&mlra_decode_workspace_bytes) f_workspace_bytes = nullptr;
 
 struct Refused {};  // a Python error is set
 
+// A reference that is given up with its scope unless it is returned.
+struct Ref {
+    PyObject* p;
+    explicit Ref(PyObject* owned) : p(owned) {}
+    Ref(const Ref&) = delete;
+    ~Ref() { Py_XDECREF(p); }
+    PyObject* release() {
+        PyObject* out = p;
+        p = nullptr;
+        return out;
+    }
+};
+
+PyObject* new_ref(PyObject* o) {
+    Py_INCREF(o);
+    return o;
+}
+
 [[noreturn]] void refuse(PyObject* type, const char* format, ...) {
     va_list ap;
     va_start(ap, format);
@@ -94,6 +112,23 @@ void* stream_of(PyObject* o, at::Device device) {
     return s;
 }
 
+// The call's output like q, when the caller gives none (a new reference).  On
+// a stream of the caller's the memory is that stream's, so that nothing still
+// queued on the current one uses it, and is not given away before the current
+// stream is done with it either.
+PyObject* output_like(const at::Tensor& q, PyObject* stream_obj, void* stream) {
+    if (stream_obj == Py_None) return THPVariable_Wrap(at::empty_like(q));
+    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(q.device().index());
+    if (current.stream() == stream) return THPVariable_Wrap(at::empty_like(q));
+    at::Tensor out;
+    {
+        const c10::cuda::CUDAStreamGuard guard(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), q.device().index()));
+        out = at::empty_like(q);
+    }
+    out.record_stream(current);
+    return THPVariable_Wrap(out);
+}
+
 void check(mlra_status st, const char* where) {
     if (st == MLRA_OK) return;
     PyObject* e = PyObject_CallFunction(g_error, "is", (int)st, where);
@@ -140,23 +175,16 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
                             pointer(a[2], "latent_cache", kBf16, {pages, P, B, dc}, dev), pointer(a[3], "rope_cache", kBf16, {pages, P, dr}, dev),
                             pointer(a[4], "block_table", kI32, {N, mp}, dev), pointer(a[5], "seqlens", kI32, {N}, dev),
                             pointer(a[6], "cu_seqlens", kI32, {N + 1}, dev)};
-        PyObject* out = a[9];
-        if (out == Py_None) out = THPVariable_Wrap(at::empty_like(q));
-        else Py_INCREF(out);
-        try {
-            void* po = pointer(out, "out", kBf16, {T, H, B, dc}, dev);
-            void* ps = a[10] == Py_None ? nullptr : pointer(a[10], "device_status", kI32, {1}, dev);
-            const mlra_dims d = {size32(N, "the batch"), size32(H, "heads"), size32(B, "branches"), size32(dc, "d_c"), size32(dr, "d_r"),
-                                 size32(P, "the page size"), size32(mp, "block_table"), size32(pages, "the pool")};
-            check(f_prefill(&d, size32(T, "the packed rows"), p[0], p[1], p[2], p[3], (const int32_t*)p[4], (const int32_t*)p[5],
-                               (const int32_t*)p[6], (float)number(a[7], "scale"), (float)number(a[8], "out_scale"), po, (int32_t*)ps,
-                               stream_of(a[11], dev)),
-                  where);
-        } catch (...) {
-            Py_DECREF(out);
-            throw;
-        }
-        return out;
+        void* stream = stream_of(a[11], dev);
+        Ref out(a[9] == Py_None ? output_like(q, a[11], stream) : new_ref(a[9]));
+        void* po = pointer(out.p, "out", kBf16, {T, H, B, dc}, dev);
+        void* ps = a[10] == Py_None ? nullptr : pointer(a[10], "device_status", kI32, {1}, dev);
+        const mlra_dims d = {size32(N, "the batch"), size32(H, "heads"), size32(B, "branches"), size32(dc, "d_c"), size32(dr, "d_r"),
+                             size32(P, "the page size"), size32(mp, "block_table"), size32(pages, "the pool")};
+        check(f_prefill(&d, size32(T, "the packed rows"), p[0], p[1], p[2], p[3], (const int32_t*)p[4], (const int32_t*)p[5],
+                        (const int32_t*)p[6], (float)number(a[7], "scale"), (float)number(a[8], "out_scale"), po, (int32_t*)ps, stream),
+              where);
+        return out.release();
     });
 }
 
@@ -226,29 +254,18 @@ PyObject* decode_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const mlra_dims d = {size32(N, "the batch"), size32(H, "heads"), size32(B, "branches"), size32(dc, "d_c"), size32(dr, "d_r"),
                              size32(P, "the page size"), size32(mp, "block_table"), size32(pages, "the pool")};
         void* stream = stream_of(a[11], dev);
-        PyObject *out = a[9], *ws = a[10];
-        if (ws != Py_None) {
-            const at::Tensor& w = tensor(ws, "workspace");
+        if (a[10] != Py_None) {
+            const at::Tensor& w = tensor(a[10], "workspace");
             if (w.device() != dev || !w.is_contiguous()) refuse(PyExc_ValueError, "workspace must be a contiguous tensor on %s", dev.str().c_str());
-            Py_INCREF(ws);
-        } else {
-            ws = default_workspace(d, dev, stream, a[11]);
         }
-        if (out == Py_None) out = THPVariable_Wrap(at::empty_like(q));
-        else Py_INCREF(out);
-        try {
-            void* po = pointer(out, "out", kBf16, {N, H, B, dc}, dev);
-            const at::Tensor& w = THPVariable_Unpack(ws);
-            check(f_decode_fp8(&d, p[0], p[1], p[2], p[3], p[4], (const int32_t*)p[5], (const int32_t*)p[6], (float)number(a[7], "scale"),
-                                  (float)number(a[8], "out_scale"), po, w.data_ptr(), w.nbytes(), stream),
-                  where);
-        } catch (...) {
-            Py_DECREF(out);
-            Py_DECREF(ws);
-            throw;
-        }
-        Py_DECREF(ws);
-        return out;
+        Ref ws(a[10] == Py_None ? default_workspace(d, dev, stream, a[11]) : new_ref(a[10]));
+        Ref out(a[9] == Py_None ? output_like(q, a[11], stream) : new_ref(a[9]));
+        void* po = pointer(out.p, "out", kBf16, {N, H, B, dc}, dev);
+        const at::Tensor& w = THPVariable_Unpack(ws.p);
+        check(f_decode_fp8(&d, p[0], p[1], p[2], p[3], p[4], (const int32_t*)p[5], (const int32_t*)p[6], (float)number(a[7], "scale"),
+                           (float)number(a[8], "out_scale"), po, w.data_ptr(), w.nbytes(), stream),
+              where);
+        return out.release();
     });
 }
 

@@ -275,6 +275,28 @@ def test_more_row_blocks_than_the_gpu_holds(branches, d_c, heads):
 
 
 @pytest.mark.gpu
+def test_output_of_a_call_on_another_stream():
+    """The output's memory is not what the current stream still works on."""
+    c = _gpu(_case(44, 16, 4, 128, 64, 64, [300], [0]))
+    want = b.mlra_prefill(**c)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    held = torch.empty_like(want)
+    keep = torch.zeros_like(want)
+    place = held.data_ptr()
+    torch.cuda._sleep(20_000_000)
+    held.fill_(5.0)  # queued behind the pause, on memory that is free for this stream now
+    keep.copy_(held)
+    del held
+    got = b.mlra_prefill(**c, stream=side)
+    assert got.data_ptr() != place
+    side.synchronize()
+    assert torch.equal(got, want)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and bool((keep == 5).all())
+
+
+@pytest.mark.gpu
 def test_two_calls_at_once():
     """Calls on two streams that share the GPU's SMs: the results of each alone."""
     one = _gpu(_case(42, 16, 4, 128, 64, 64, [700, 300], [0, 200]))

@@ -14,10 +14,12 @@
 // conversion.  B has to be 8 bits then too, which a query or a probability is
 // not; but N is free until the columns cost as much as A does (N = 64 at
 // M = 128), so each is split into parts that stand side by side in N:
-//  - a query value, scaled so that the sequence's largest is at most 448,
-//    into hi + lo, both e4m3: 4 + 4 significant bits carry bf16's 8; what the
-//    smallest values lose is 2^-10 of a unit of which the largest has 224 or
-//    more, 2^-17.8 of it.  S = S_hi + S_lo, added when the scores are read.
+//  - a query value, scaled so that the largest of its head and branch is at
+//    most 448, into hi + lo, both e4m3: 4 + 4 significant bits carry bf16's 8;
+//    what the smallest values lose is 2^-10 of a unit of which the largest has
+//    224 or more, 2^-17.8 of it.  S = S_hi + S_lo, added when the scores are
+//    read; the units are factors of the columns, so that a head's accuracy
+//    depends on no other head or branch.
 //  - a probability into three e5m2 parts: each takes the leading 3 bits of
 //    what is left (the upper byte of a half is an e5m2 value), the last one
 //    rounded: 9 significant bits, 2^-9 of it.  e5m2 because its exponent is
@@ -106,7 +108,7 @@ struct Cfg {
     static constexpr int P_PART_BYTES = kT * kHP;                // one part of one branch
     static constexpr int P_BRANCH_BYTES = 3 * P_PART_BYTES;
     static constexpr int P_BYTES = SBR * P_BRANCH_BYTES;
-    static constexpr int MISC_BYTES = 2048;
+    static constexpr int MISC_BYTES = 3072;
     // steps between their score MMA and their output MMA (a tile's and one
     // more); RoPE tiles in flight (more where a tile is a chunk or two); RoPE
     // score slots (one is written again when the steps that read it are over)
@@ -114,7 +116,7 @@ struct Cfg {
     static constexpr int NROPE = NCH >= 4 ? 2 : NCH == 2 ? 3 : 4;
     static constexpr int NRS = (NSP + 2 * NSTEP - 2) / NSTEP > 2 ? (NSP + 2 * NSTEP - 2) / NSTEP : 2;
     static constexpr int FIXED = NROPE * ROPE_BYTES + Q_BYTES + QR_SPAN + NSP * P_BYTES + MISC_BYTES;
-    static constexpr int NSTAGE_FIT = (kSmemLimit - 1024 - FIXED) / CHUNK_BYTES;
+    static constexpr int NSTAGE_FIT = (kSmemLimit - FIXED) / CHUNK_BYTES;
     static constexpr int NSTAGE = NSTAGE_FIT > kMaxStages ? kMaxStages : NSTAGE_FIT;
     static constexpr int OFF_CHUNK = 0;
     static constexpr int OFF_ROPE = OFF_CHUNK + NSTAGE * CHUNK_BYTES;
@@ -122,7 +124,7 @@ struct Cfg {
     static constexpr int OFF_QR = OFF_Q + Q_BYTES;
     static constexpr int OFF_P = OFF_QR + QR_SPAN;
     static constexpr int OFF_MISC = OFF_P + NSP * P_BYTES;
-    static constexpr int SMEM_BYTES = OFF_MISC + MISC_BYTES + 1024;
+    static constexpr int SMEM_BYTES = OFF_MISC + MISC_BYTES;
     // TMEM columns: output blocks, score slots, RoPE score slots
     static constexpr int O_BLOCKS = NCH * BPC;
     static constexpr int S_COL0 = O_BLOCKS * kPN;
@@ -154,13 +156,13 @@ struct Misc {
     int plan[4];
     int last_seg[4];
     int merge_flag;
-    float q_max[4 * kGroups];     // largest query magnitude seen by each softmax warp
     uint8_t raise[kGroups][2];    // tile t (t & 1): some warp of the group needs a higher reference
     float red[kGroups][4][kHP];       // [group][quadrant][head]: maxima of a raise, at the end sums
     alignas(16) float m_run[kGroups][kHP];  // references M; read as float4
+    alignas(16) float q_unit[2][4 * kHP];   // range k in place k % 2: unit of the queries of each [branch][head]
     float factor[kGroups][kHP];       // a raise: what O and l shrink by; at the end 1 / l
 };
-static_assert(offsetof(Misc, m_run) % 16 == 0, "float4 access");
+static_assert(offsetof(Misc, m_run) % 16 == 0 && offsetof(Misc, q_unit) % 16 == 0, "float4 access");
 
 struct Maps {
     CUtensorMap lat;   // latent bytes [pages * P][W]
@@ -206,8 +208,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                   const float* __restrict__ latent_scale, const int whole) {
     using C = Cfg<NB, DC, DR>;
     static_assert(sizeof(Misc) <= C::MISC_BYTES, "barriers and scratch fit the MISC region");
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t sm[];  // (the swizzle atoms start at 1024 bytes)
     Misc& misc = *reinterpret_cast<Misc*>(sm + C::OFF_MISC);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int P = a.page_size;
@@ -518,16 +519,17 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
             const int row = quad * 32 + lane;                // token (S) / latent column (O); also the thread's number in the group
             const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
             const int H = a.heads, log_p = __ffs(P) - 1;     // (P is a power of two)
-            uint32_t tcnt = 0;
+            uint32_t tcnt = 0, ranges = 0;
             bool dead = false;
             int pend_a = -1, pend_b = -1;
 
             // A range: its tiles, and what this thread has in hand when they begin:
-            // its token's page one tile ahead, its scale, and the query unit.
+            // its token's page one tile ahead, its scale, and its heads' query units.
             struct Range {
                 int n, cum, L, tiles, tb, te;
                 int page_next;
-                float sig, alpha_q;
+                float sig;
+                const float* unit;
                 bool bad;
             };
             auto page_of = [&](const Range& r, int j) {
@@ -550,20 +552,20 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                 // 16 head rows; heads past the last are zero
                 constexpr int UPR = C::W / 8;               // 8-value units per head row
                 constexpr int UNITS = kHP * UPR;
-                constexpr int U = (UNITS + kSoft - 1) / kSoft;
-                const int sid = threadIdx.x - 128;
-                const __nv_bfloat16* q = a.q_lat + ((size_t)r.n * H + grp.h0) * C::W;
+                constexpr int U = (UNITS + kSoft - 1) / kSoft;  // units of a thread, side by side
+                constexpr int SEG = DC / 8 / U;             // threads of one head and branch
+                static_assert(SEG <= 32 && SEG * U * 8 == DC, "a warp has whole heads of a branch");
+                const int sid = threadIdx.x - 128, h = sid * U / UPR, u0 = sid * U % UPR;
+                const bool some = sid * U < UNITS && h < grp.hn;
+                const uint4* q = reinterpret_cast<const uint4*>(a.q_lat + ((size_t)r.n * H + grp.h0 + h) * C::W) + u0;
                 uint4 v[U];
 #pragma unroll
-                for (int i = 0; i < U; ++i) {
-                    const int u = sid + kSoft * i;
-                    v[i] = u < UNITS && u / UPR < grp.hn ? __ldg(reinterpret_cast<const uint4*>(q + (size_t)(u / UPR) * C::W) + u % UPR)
-                                                         : make_uint4(0u, 0u, 0u, 0u);
-                }
+                for (int i = 0; i < U; ++i) v[i] = some ? __ldg(q + i) : make_uint4(0u, 0u, 0u, 0u);
                 constexpr int RU = DR / 8;                  // 16-byte units of a RoPE row
                 uint4 rv = make_uint4(0u, 0u, 0u, 0u);
                 if (sid < kHP * RU && sid / RU < grp.hn)
                     rv = __ldg(reinterpret_cast<const uint4*>(a.q_rope + ((size_t)r.n * H + grp.h0 + sid / RU) * DR) + sid % RU);
+                // the largest finite magnitude of the head and branch, as 16-bit integers
                 uint32_t mx = 0;
 #pragma unroll
                 for (int i = 0; i < U; ++i) {
@@ -575,8 +577,16 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                         mx = max(mx, hi < 0x7f80u ? hi : 0u);
                     }
                 }
-                mx = __reduce_max_sync(0xffffffffu, mx);
-                if (lane == 0) misc.q_max[warp - 4] = __uint_as_float(mx << 16);
+#pragma unroll
+                for (int o = SEG / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                // their unit: the smallest power of two tau with mx <= 448 tau (2^-100 at
+                // least: both it and its reciprocal are normal numbers)
+                const int e = max((int)(mx >> 7) - 135 + ((mx & 0x7fu) > 0x60u), -100);
+                const float inv_tau = __uint_as_float((uint32_t)(127 - e) << 23);
+                // (the other place holds the units of the range that slower groups are in)
+                float* unit = misc.q_unit[ranges++ & 1];
+                if (sid * U < UNITS && sid % SEG == 0) unit[u0 * 8 / DC * kHP + h] = __uint_as_float((uint32_t)(127 + e) << 23);
+                r.unit = unit + br * kHP + hoff;
                 // (every group comes here for every range, also one that has given up:
                 // then all stop)
                 if (named_bar_or<5, kSoft>(dead)) {
@@ -584,25 +594,13 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                     return false;
                 }
                 r.sig = scale_of(r, page, r.tb);
-                // (q_max is written again after this range's tiles, whose scores wait for
-                // every warp's q_full)
-                float top = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4 * kGroups; ++i) top = fmaxf(top, misc.q_max[i]);
-                // the smallest power of two tau with top <= 448 tau (2^-100 at least: both it
-                // and its reciprocal are normal numbers); a score of the MMA times alpha_q is
-                // in log2 units (without sigma)
-                const uint32_t bits = __float_as_uint(top);
-                const int e = max((int)(bits >> 23) - 135 + ((bits & 0x7fffffu) > 0x600000u), -100);
-                const float inv_tau = __uint_as_float((uint32_t)(127 - e) << 23);
-                r.alpha_q = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
                 if (sid < kHP * RU) {
                     const int h = sid / RU, u = sid % RU;
                     *reinterpret_cast<uint4*>(sm + C::OFF_QR + (DR == 64 ? h * 128 + ((u ^ (h & 7)) << 4) : h * 64 + ((u ^ ((h >> 1) & 3)) << 4))) = rv;
                 }
 #pragma unroll
                 for (int i = 0; i < U; ++i) {
-                    const int u = sid + kSoft * i, h = u / UPR, col = u % UPR * 8;
+                    const int col = (u0 + i) * 8;
                     const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
                     uint32_t hi[4], lo[4];
 #pragma unroll
@@ -614,7 +612,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                         const float2 f = from_e4m3x2(hi[k]);
                         lo[k] = e4m3x2(x - f.x, y - f.y);
                     }
-                    if (u < UNITS) {
+                    if (sid * U < UNITS) {
                         uint8_t* dst = sm + C::OFF_Q + col / 128 * C::Q_CHUNK_BYTES + h * 128 +
                                        (((col % 128 / 16) ^ (h & 7)) << 4) + col % 16;
                         *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
@@ -631,7 +629,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
             bool more = begin_range(rg);
             while (more) {  // (a group that has given up goes on to the barrier in begin_range)
                 const int tb = rg.tb, te = rg.te;
-                const float alpha_q = rg.alpha_q;
+                const float* unit = rg.unit;
                 int page_next = rg.page_next;
                 float sig = rg.sig, sig_next = 0.f;
                 float l[HG];  // this thread's share of sum w / sigma
@@ -644,7 +642,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                     const int page_after = page_of(rg, j + 2);
                     if (j + 1 < te) sig_next = scale_of(rg, page_next, j + 1);
                     page_next = page_after;
-                    const float ls = fast_log2(sig), k = sig * alpha_q;
+                    const float ls = fast_log2(sig), k = sig * a.scale_log2;  // a score of the MMAs times k and its unit is in log2 units
                     const float rs = masked ? 0.f : __frcp_rn(sig);
                     // z: log2 of p sigma per head
                     float z[HG];
@@ -660,7 +658,13 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                             tmem_ld_cols<N>(s_at + kHP + i0, low);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < N; ++i) z[i0 + i] = fmaf(hi[i] + low[i], k, fmaf(r[i], a.scale_log2, ls));
+                            for (int i = 0; i < N; i += 4) {
+                                const float4 t = *reinterpret_cast<const float4*>(unit + i0 + i);
+                                const float tau[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                                for (int u = 0; u < 4; ++u)
+                                    z[i0 + i + u] = fmaf(hi[i + u] + low[i + u], k * tau[u], fmaf(r[i + u], a.scale_log2, ls));
+                            }
                         }
                         if (masked) {
 #pragma unroll

@@ -386,7 +386,7 @@ MLRA_API mlra_status mlra_append_fp8(const mlra_dims* dims, int32_t tokens, cons
  *                (mlra_append_fp8 writes powers of two from 2^-40 on)
  * The queries, scores, sums and outputs keep mlra_decode's precision: only
  * the cache is in 8 bits.  (Queries enter the products as two e4m3 parts, 2^-17
- * of the sequence's largest query value; probabilities as three e5m2 parts,
+ * of the largest value of their head and branch; probabilities as three e5m2 parts,
  * 2^-9 of each.)
  */
 MLRA_API mlra_status mlra_decode_fp8(const mlra_dims* dims, const void* q_lat, const void* q_rope,

@@ -155,19 +155,38 @@ def mlra_decode_workspace_bytes(dims: mlra_dims, num_ctas: int = 0) -> int:
     return int(n)
 
 
+# The default workspaces, by (device index, stream handle, capture id or 0): a
+# call without a workspace uses its stream's, and under graph capture one of
+# the capture's own, so that neither calls on different streams nor replays of
+# different graphs share one.  A capture's (graph pool memory, its zeroing
+# captured too) stays here until the next capture on that stream.
 _ws_cache = {}
+_WS_HEAD = 256 + 4 * 65536  # the error word and the split counters, the part that must start at zero
 
 
-def workspace_for(dims: mlra_dims, device: torch.device) -> torch.Tensor:
-    """A zeroed workspace of the required size, cached per device and grown
-    on demand.  Calls sharing it must not overlap on the GPU."""
-    need = mlra_decode_workspace_bytes(dims)
-    key = device.index if device.index is not None else torch.cuda.current_device()
-    ws = _ws_cache.get(key)
-    if ws is None or ws.numel() < need:
-        ws = torch.zeros(need, dtype=torch.uint8, device=device)
-        _ws_cache[key] = ws
+def _new_workspace(need: int, key, stream) -> torch.Tensor:
+    """A first, or larger, default workspace for `key`; `stream`: the call's
+    (None: the current one)."""
+    index, handle, capture = key
+    with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(index)):
+        ws = torch.empty(max(need, _WS_HEAD), dtype=torch.uint8, device=torch.device("cuda", index))
+        ws[:_WS_HEAD].zero_()
+    if capture:
+        for k in [k for k in _ws_cache if k[:2] == key[:2] and k[2] not in (0, capture)]:
+            del _ws_cache[k]
+    _ws_cache[key] = ws
     return ws
+
+
+def _index(device: torch.device) -> int:
+    return device.index if device.index is not None else torch.cuda.current_device()
+
+
+def workspace_for(dims: mlra_dims, device: torch.device, stream=None) -> torch.Tensor:
+    """The default workspace of a call with `dims` on `stream` (None: the
+    current one): kept per device and stream, one for each graph capture, and
+    grown on demand."""
+    return _launches().workspace(mlra_decode_workspace_bytes(dims), _index(device), stream)
 
 
 def _decode(entry, q_lat, q_rope, latent_cache, rope_cache, block_table, seqlens, scale, out_scale,
@@ -200,7 +219,7 @@ def _decode_call(call, name, q_lat, q_rope, latent_cache, rope_cache, block_tabl
         if out.shape != q_lat.shape:
             raise ValueError("out must have the shape of q_lat")
     if workspace is None:
-        workspace = workspace_for(dims, dev)
+        workspace = workspace_for(dims, dev, stream)
     st = call(ctypes.byref(dims), _ptr(q_lat), _ptr(q_rope), _ptr(latent_cache), _ptr(rope_cache),
               _ptr(block_table), _ptr(seqlens), float(scale), float(out_scale), _ptr(out), _ptr(workspace),
               workspace.numel() * workspace.element_size(), _stream_ptr(stream, dev))
@@ -215,6 +234,9 @@ def mlra_decode(q_lat, q_rope, latent_cache, rope_cache, block_table, seqlens, s
     q_lat bf16 [N,H,B,d_c], q_rope bf16 [N,H,d_r], latent_cache bf16
     [pages,P,B,d_c], rope_cache bf16 [pages,P,d_r], block_table int32
     [N,max_pages], seqlens int32 [N]; returns out bf16 [N,H,B,d_c].
+    Without a workspace the call uses its stream's, and under graph capture one
+    of the capture's own, whose head every replay zeroes (pass a workspace to
+    save that, or to read a replay's device error after another capture).
     """
     return _decode("mlra_decode", q_lat, q_rope, latent_cache, rope_cache, block_table, seqlens,
                    scale, out_scale, out, workspace, stream)
@@ -310,24 +332,25 @@ def _up_proj(out_lat, w_uv, gate, d_h, y, stream) -> torch.Tensor:
     return y
 
 
-def default_workspace(device: Optional[torch.device] = None) -> Optional[torch.Tensor]:
-    """The cached workspace that decode calls without an explicit workspace
-    use on `device` (None if none has been made yet)."""
+def default_workspace(device: Optional[torch.device] = None, stream=None) -> Optional[torch.Tensor]:
+    """The workspace that decode calls without an explicit one use on `device`
+    and `stream` (None: the current one) outside graph capture; None if none
+    has been made yet."""
     dev = device if device is not None else torch.device("cuda", torch.cuda.current_device())
-    key = dev.index if dev.index is not None else torch.cuda.current_device()
-    return _ws_cache.get(key)
+    return _ws_cache.get((_index(dev), _stream_ptr(stream, dev), 0))
 
 
 def mlra_read_device_error(workspace: Optional[torch.Tensor] = None, stream=None) -> int:
     """Synchronise the stream; return and clear the device error code of
-    `workspace` (default: the cached workspace of the current device, then the
-    one that mlra_decode_fp8 keeps for this stream).  A reported
+    `workspace` (default: the first code found in the current device's default
+    workspaces, this stream's before the others').  A reported
     MLRA_ERR_DEVICE_TIMEOUT also clears the workspace's split counters, so the
     workspace serves the next call."""
     if workspace is None:
         dev = torch.device("cuda", torch.cuda.current_device())
-        for ws in (default_workspace(dev), _ws_cache.get((dev.index, _stream_ptr(stream, dev)))):
-            code = MLRA_OK if ws is None else mlra_read_device_error(ws, stream)
+        here = (dev.index, _stream_ptr(stream, dev))
+        for key in sorted((k for k in _ws_cache if k[0] == dev.index), key=lambda k: k[:2] != here):
+            code = mlra_read_device_error(_ws_cache[key], stream)
             if code != MLRA_OK:
                 return code
         return MLRA_OK
@@ -426,27 +449,6 @@ def _launches():
     return _launch_module
 
 
-_WS_HEAD = 256 + 4 * 65536  # the error word and the split counters, the part that must start at zero
-
-
-def _new_workspace(need: int, index: int, stream) -> torch.Tensor:
-    """A first, or larger, default workspace of a call on `stream` (None: the
-    current one): mlra_decode's own on the legacy default stream, one for each
-    other stream, and one for each call under graph capture, so that neither
-    calls on different streams nor replays of different graphs share one."""
-    s = stream if stream is not None else torch.cuda.current_stream(index)
-    with torch.cuda.stream(s):
-        capturing = torch.cuda.is_current_stream_capturing()
-        key = index if s.cuda_stream == 0 else (index, s.cuda_stream)
-        ws = None if capturing else _ws_cache.get(key)
-        if ws is None or ws.numel() < need:
-            ws = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
-            ws[:_WS_HEAD].zero_()
-            if not capturing:
-                _ws_cache[key] = ws
-    return ws
-
-
 def mlra_prefill(q_lat, q_rope, latent_cache, rope_cache, block_table, seqlens, cu_seqlens, scale, out_scale,
                  out=None, device_status=None, stream=None) -> torch.Tensor:
     """Causal attention of packed new tokens over the paged cache, every
@@ -488,9 +490,7 @@ def mlra_decode_fp8(q_lat, q_rope, latent_cache, latent_scale, rope_cache, block
     q_lat bf16 [N,H,B,d_c], q_rope bf16 [N,H,d_r], latent_cache float8_e4m3fn
     [pages,P,B,d_c], latent_scale fp32 [pages,P/16,B], rope_cache bf16
     [pages,P,d_r], block_table int32 [N,max_pages], seqlens int32 [N]; returns
-    out bf16 [N,H,B,d_c].  Without a workspace the call uses one of its
-    stream's (under graph capture one of its own: pass a workspace there to be
-    able to read the device error of a replay).
+    out bf16 [N,H,B,d_c].  The workspace is as in mlra_decode.
     """
     return _launches().decode_fp8(q_lat, q_rope, latent_cache, latent_scale, rope_cache, block_table, seqlens, scale,
                                   out_scale, out, workspace, stream)

@@ -10,8 +10,8 @@
 #include <Python.h>
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAGuard.h>
-#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAStream.h>
+#include <cuda_runtime_api.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdarg>
@@ -215,24 +215,35 @@ PyObject* append_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// The default workspace on `stream`: the cached one, or what binding.py makes
-// (a first or larger one, or a capture's own).  A new reference.
-PyObject* default_workspace(const mlra_dims& d, at::Device dev, void* stream, PyObject* stream_obj) {
-    const size_t need = f_workspace_bytes(&d, 0);
-    if (need == 0) check(MLRA_ERR_INVALID_ARG, "mlra_decode_workspace_bytes");
-    if (stream_obj == Py_None && c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None) {
-        PyObject* key = stream == nullptr ? PyLong_FromLong(dev.index()) : Py_BuildValue("iN", (int)dev.index(), PyLong_FromVoidPtr(stream));
-        if (key == nullptr) throw Refused{};
-        PyObject* ws = PyDict_GetItem(g_workspaces, key);  // borrowed
-        Py_DECREF(key);
-        if (ws != nullptr && THPVariable_Check(ws) && THPVariable_Unpack(ws).nbytes() >= need) {
-            Py_INCREF(ws);
-            return ws;
-        }
-    }
-    PyObject* ws = PyObject_CallFunction(g_workspace_fn, "niO", (Py_ssize_t)need, (int)dev.index(), stream_obj);
+// The default workspace of a call on `stream` that needs `need` bytes: the one
+// kept for (device, stream, capture id or 0), or a first or larger one that
+// binding.py makes.  A new reference.
+PyObject* default_workspace(size_t need, at::Device dev, void* stream, PyObject* stream_obj) {
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    C10_CUDA_CHECK(cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &status, &id));
+    if (status == cudaStreamCaptureStatusNone) id = 0;
+    Ref key(Py_BuildValue("iNK", (int)dev.index(), PyLong_FromVoidPtr(stream), id));
+    if (key.p == nullptr) throw Refused{};
+    PyObject* kept = PyDict_GetItemWithError(g_workspaces, key.p);  // borrowed
+    if (kept == nullptr && PyErr_Occurred()) throw Refused{};
+    if (kept != nullptr && THPVariable_Check(kept) && THPVariable_Unpack(kept).nbytes() >= need) return new_ref(kept);
+    PyObject* ws = PyObject_CallFunction(g_workspace_fn, "nOO", (Py_ssize_t)need, key.p, stream_obj);
     if (ws == nullptr) throw Refused{};
     return ws;
+}
+
+// (bytes, device index, stream): the default workspace of a call on that stream
+PyObject* workspace(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!expects(n, 3, "workspace")) return nullptr;
+    return guarded([&]() -> PyObject* {
+        const size_t need = PyLong_AsSize_t(a[0]);
+        const long index = PyLong_AsLong(a[1]);
+        if (PyErr_Occurred()) throw Refused{};
+        const at::Device dev(at::kCUDA, (at::DeviceIndex)index);
+        const c10::cuda::OptionalCUDAGuard guard(dev);
+        return default_workspace(need, dev, stream_of(a[2], dev), a[2]);
+    });
 }
 
 // (q_lat, q_rope, latent_cache, latent_scale, rope_cache, block_table, seqlens, scale, out_scale, out, workspace, stream)
@@ -258,7 +269,9 @@ PyObject* decode_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
             const at::Tensor& w = tensor(a[10], "workspace");
             if (w.device() != dev || !w.is_contiguous()) refuse(PyExc_ValueError, "workspace must be a contiguous tensor on %s", dev.str().c_str());
         }
-        Ref ws(a[10] == Py_None ? default_workspace(d, dev, stream, a[11]) : new_ref(a[10]));
+        const size_t need = a[10] == Py_None ? f_workspace_bytes(&d, 0) : 1;
+        if (need == 0) check(MLRA_ERR_INVALID_ARG, "mlra_decode_workspace_bytes");
+        Ref ws(a[10] == Py_None ? default_workspace(need, dev, stream, a[11]) : new_ref(a[10]));
         Ref out(a[9] == Py_None ? output_like(q, a[11], stream) : new_ref(a[9]));
         void* po = pointer(out.p, "out", kBf16, {N, H, B, dc}, dev);
         const at::Tensor& w = THPVariable_Unpack(ws.p);
@@ -289,6 +302,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef methods[] = {{"prefill", MLRA_FAST(prefill), nullptr},
                          {"append_fp8", MLRA_FAST(append_fp8), nullptr},
                          {"decode_fp8", MLRA_FAST(decode_fp8), nullptr},
+                         {"workspace", MLRA_FAST(workspace), nullptr},
                          {"bind", MLRA_FAST(bind), nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_launch", "Checked launches of the prompt and 8-bit cache entry points.", -1, methods};

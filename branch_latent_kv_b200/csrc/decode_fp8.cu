@@ -25,7 +25,7 @@
 //    rounded: 9 significant bits, 2^-9 of it.  e5m2 because its exponent is
 //    fp16's; the second and third part are scaled up by 2^2 and 2^5 (their
 //    columns are summed apart), so that nothing above 2^-22 is lost: with the
-//    largest weight at 2^2 .. 2^15 that is 2^-24 of it, and long flat tails are
+//    largest weight at 2^7 .. 2^15 that is 2^-29 of it, and long flat tails are
 //    made of such weights.
 // The value scales go into the probabilities:
 //   z_t = log2(e) scale s_t + log2 sigma_t,  w_t = 2^(z_t - M) = p_t sigma_t,
@@ -72,8 +72,13 @@ constexpr int kPN = 3 * kHP;  // output columns of a block: three probability pa
 constexpr int kMaxStages = 9;
 constexpr int kMaxSteps = 5;
 // the reference M sits 2^kBase below the largest weight when it is set, and is
-// raised when a weight passes 2^kTop (e5m2 holds 1.75 2^15)
-constexpr float kBase = 2.0f, kTop = 15.0f;
+// raised when a weight passes 2^kTop (e5m2 holds 1.75 2^15).  The higher kBase,
+// the smaller the weights that count (2^-22 is what is left of them), and the
+// more raises: at scores of a standard deviation of 2, 16 x 8192 tokens take
+// 34.5 us with 2 to 8, the ragged batch 96.3 to 96.6 us.  With 2, 2^18 tokens
+// 2^24.5 below one of no value came out as zero.  (No power of two: where fp32's
+// step is 16, a largest score less 8 can round to 16 below it, a weight of 2^16.)
+constexpr float kBase = 7.0f, kTop = 15.0f;
 // Contexts of up to this many tiles are not split: 64 x 500 tokens of four
 // branches 17.5 us against 24.3 us split, 1 x 256 of the tiny shape 10.0 against
 // 14.4; at eight tiles 4 x 1000 tokens take 26.2 us against 17.4 us split.

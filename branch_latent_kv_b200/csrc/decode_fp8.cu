@@ -25,8 +25,8 @@
 //    rounded: 9 significant bits, 2^-9 of it.  e5m2 because its exponent is
 //    fp16's; the second and third part are scaled up by 2^2 and 2^5 (their
 //    columns are summed apart), so that nothing above 2^-22 is lost: with the
-//    largest weight at 2^7 .. 2^15 that is 2^-29 of it, and long flat tails are
-//    made of such weights.
+//    largest weight at 2^2 .. 2^15 that is 2^-24 of it, in long ranges, whose flat
+//    tails are made of such weights, down to 2^-29.
 // The value scales go into the probabilities:
 //   z_t = log2(e) scale s_t + log2 sigma_t,  w_t = 2^(z_t - M) = p_t sigma_t,
 //   o = sum w_t e_t / l,  l = sum w_t / sigma_t,
@@ -71,14 +71,16 @@ constexpr int kSN = 2 * kHP;  // score columns of a branch: hi and lo query part
 constexpr int kPN = 3 * kHP;  // output columns of a block: three probability parts
 constexpr int kMaxStages = 9;
 constexpr int kMaxSteps = 5;
-// the reference M sits 2^kBase below the largest weight when it is set, and is
-// raised when a weight passes 2^kTop (e5m2 holds 1.75 2^15).  The higher kBase,
-// the smaller the weights that count (2^-22 is what is left of them), and the
-// more raises: at scores of a standard deviation of 2, 16 x 8192 tokens take
-// 34.5 us with 2 to 8, the ragged batch 96.3 to 96.6 us.  With 2, 2^18 tokens
-// 2^24.5 below one of no value came out as zero.  (No power of two: where fp32's
-// step is 16, a largest score less 8 can round to 16 below it, a weight of 2^16.)
-constexpr float kBase = 7.0f, kTop = 15.0f;
+// The reference M sits 2^base below the largest weight when it is set, and is
+// raised when a weight passes 2^kTop (e5m2 holds 1.75 2^15).  What is left of a
+// weight ends at 2^-22, so a range of n tokens leaves out n 2^-(22 + base) of its
+// largest weight at most: base is log2 n - 11, from 2 (n = 2^13) to kBaseMost.  It is no higher than that asks for, since raises cost: 16 x 8192
+// tokens 32.7 us with 2, 33.9 with 5, 34.6 with 8, the ragged batch 94.9, 96.6,
+// 99.5.  With 2 throughout, 2^18 tokens 2^24.5 below one of no value came out as
+// zero.  (kBaseMost is no 8: where fp32's step is 16, a largest score less 8 can
+// round to 16 below it, a weight of 2^16.)
+constexpr float kTop = 15.0f;
+constexpr int kBaseMost = 7;
 // Contexts of up to this many tiles are not split: 64 x 500 tokens of four
 // branches 17.5 us against 24.3 us split, 1 x 256 of the tiny shape 10.0 against
 // 14.4; at eight tiles 4 x 1000 tokens take 26.2 us against 17.4 us split.
@@ -582,6 +584,8 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                         mx = max(mx, hi < 0x7f80u ? hi : 0u);
                     }
                 }
+                if constexpr (SEG == 32) mx = __reduce_max_sync(0xffffffffu, mx);
+                else
 #pragma unroll
                 for (int o = SEG / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                 // their unit: the smallest power of two tau with mx <= 448 tau (2^-100 at
@@ -635,6 +639,11 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
             while (more) {  // (a group that has given up goes on to the barrier in begin_range)
                 const int tb = rg.tb, te = rg.te;
                 const float* unit = rg.unit;
+                // (four units stay in registers: one 512-wide branch 72.4 us against 74.0; with
+                // eight or sixteen heads they cost more there: 16 x 8192 tokens 35.0 us from 32.8)
+                float tau4[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tau4[i] = unit[i];
                 int page_next = rg.page_next;
                 float sig = rg.sig, sig_next = 0.f;
                 float l[HG];  // this thread's share of sum w / sigma
@@ -657,19 +666,15 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                         const uint32_t r_at = lanes + C::R_COL0 + (tcnt % C::NRS) * kHP + hoff;
 #pragma unroll
                         for (int i0 = 0; i0 < HG; i0 += N) {
-                            float hi[N], low[N], r[N];
+                            float tau[N], hi[N], low[N], r[N];
+#pragma unroll
+                            for (int i = 0; i < N; ++i) tau[i] = HG == 4 ? tau4[i] : unit[i0 + i];
                             tmem_ld_cols<N>(r_at + i0, r);
                             tmem_ld_cols<N>(s_at + i0, hi);
                             tmem_ld_cols<N>(s_at + kHP + i0, low);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < N; i += 4) {
-                                const float4 t = *reinterpret_cast<const float4*>(unit + i0 + i);
-                                const float tau[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-                                for (int u = 0; u < 4; ++u)
-                                    z[i0 + i + u] = fmaf(hi[i + u] + low[i + u], k * tau[u], fmaf(r[i + u], a.scale_log2, ls));
-                            }
+                            for (int i = 0; i < N; ++i) z[i0 + i] = fmaf(hi[i] + low[i], k * tau[i], fmaf(r[i], a.scale_log2, ls));
                         }
                         if (masked) {
 #pragma unroll
@@ -753,8 +758,9 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                         if (row == 0) misc.raise[sg][tcnt & 1] = 0;  // (all have read it before the barrier above)
                         named_bar_sync_id<128>(gbar);
                         if (row < HG) {
+                            const int base = min(max(28 - __clz(te - tb - 1), 2), kBaseMost);  // log2 of the range's tokens less 11
                             const float t = fmaxf(fmaxf(misc.red[sg][0][row], misc.red[sg][1][row]),
-                                                  fmaxf(misc.red[sg][2][row], misc.red[sg][3][row])) - kBase;
+                                                  fmaxf(misc.red[sg][2][row], misc.red[sg][3][row])) - (float)base;
                             const float m = misc.m_run[sg][row], mnew = j == tb ? t : fmaxf(m, t);
                             misc.factor[sg][row] = j == tb ? 1.f : fast_exp2(m - mnew);
                             misc.m_run[sg][row] = mnew;  // (all have read the old one before the barrier above)

@@ -387,8 +387,9 @@ MLRA_API mlra_status mlra_append_fp8(const mlra_dims* dims, int32_t tokens, cons
  * The queries, scores, sums and outputs keep mlra_decode's precision: only
  * the cache is in 8 bits.  (Queries enter the products as two e4m3 parts, 2^-17
  * of the largest value of their head and branch; probabilities as three e5m2 parts,
- * 2^-9 of each or 2^-29 of the largest product of one and its scale; a product
- * 2^-133 of the largest or less counts as none, in the sum of the weights too.)
+ * 2^-9 of each or, in all of a CTA's range of a sequence, 2^-11 of its largest
+ * product of a probability and its scale, up to 2^18 tokens; a product 2^-128 of
+ * the largest or less counts as none, in the sum of the probabilities too.)
  */
 MLRA_API mlra_status mlra_decode_fp8(const mlra_dims* dims, const void* q_lat, const void* q_rope,
                                      const void* latent_cache, const void* latent_scale, const void* rope_cache,

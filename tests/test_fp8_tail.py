@@ -3,8 +3,9 @@ one, in a single CTA's range: what three e5m2 parts leave of such a weight.
 
 A weight w = p sigma / 2^M is rounded to fp16 and then to 2^-21, the step of
 the third part's smallest values: off by at most 2^-22 + 2^-25 wherever that is
-more than R_PROB of it.  The largest weight of a range is 2^7 or more, so the
-weight's error is at most 1.125 2^-29 of that one."""
+more than R_PROB of it.  The largest weight of a range of n tokens, 2^13 <= n <=
+2^18, is n 2^-11 or more, so the errors of its weights add up to at most 1.125
+2^-11 of that one: 1.125 2^-29 for each of 2^18 tokens."""
 import math
 
 import pytest

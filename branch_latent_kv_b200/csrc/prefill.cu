@@ -36,7 +36,7 @@
 // next block's queries, first tiles and first scores come while this one's
 // last softmax and its output are under way.  Prompts of 1 to 1024 tokens, 612
 // blocks: 49 us, where a new CTA for every block cost 12 us more.  (Where a block's
-// tokens are split, all blocks run at once and each CTA has one.)
+// tokens are split, each CTA has one block.)
 //
 // What the widths ask for, with what it measured:
 //  - d_c <= 128: tiles of 128 x 128 scores, a row of them in one thread's
@@ -1059,8 +1059,14 @@ cudaError_t launch_cfg(const PrefillArgs& a, cudaStream_t stream) {
     // idle, a row block's tokens are split over a cluster of up to 8 CTAs, four
     // tiles each at least (by the block table, which bounds the lengths) and as
     // many clusters as the device holds at once (a cluster stays within a group of
-    // SMs).  One new token after 8191: 28.8 us in 8 parts, 42 in 4, 129 in one;
-    // 4 x 16 tokens after 8192: 48 us in 4 parts, 65 in 8 (two waves), 135 in one.
+    // SMs: 74 clusters of 2, 33 of 4, 15 of 8).  One new token after 8191: 30.5 us in
+    // 8 parts, 136 in one.  Every sequence has row blocks of its own; the lengths of
+    // the runs are not known here, so their average stands for them.  One new token
+    // in each of 8, 32, 64 sequences after 8191: 52, 153, 328 us, where the blocks of
+    // all rows laid end to end, with more parts, gave 95, 296, 442 (of 1 to 7 tokens
+    // after up to 8191: 42, 152, 245 us and 70, 148, 226).  Pairs may be a quarter more
+    // than fit at once: 16 sequences of the 512-wide branch in 4 parts take 132 us
+    // at one token after 8191 each, 67 ragged, in 2 parts 122 and 117.
     static const auto resident = [&] {
         std::array<int, 4> n{};  // clusters of 1, 2, 4, 8 CTAs
         cudaLaunchConfig_t c = cfg;
@@ -1073,10 +1079,12 @@ cudaError_t launch_cfg(const PrefillArgs& a, cudaStream_t stream) {
         cudaGetLastError();
         return n;
     }();
-    const long long blocks = (long long)((q_rows + C::BM - 1) / C::BM) * a.branches;
+    const long long runs = a.batch < a.tokens ? a.batch : a.tokens;  // sequences with new tokens, at most
+    const long long rows_of_run = (a.tokens + runs - 1) / runs * a.heads;
+    const long long blocks = runs * ((rows_of_run + C::BM - 1) / C::BM) * a.branches;
     const long long most = (long long)a.max_pages * a.page_size / (4 * C::KT);
     int log_splits = 0;
-    while (C::NV << log_splits < 8 && blocks <= resident[log_splits + 1 + (C::NV == 2)] && 2 << log_splits <= most) ++log_splits;
+    while (C::NV << log_splits < 8 && blocks * 4 <= resident[log_splits + 1 + (C::NV == 2)] * (C::PAIR ? 5 : 4) && 2 << log_splits <= most) ++log_splits;
     const long long grid = places * a.branches * C::NV << log_splits;
     if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
     cfg.gridDim = dim3((unsigned)grid);

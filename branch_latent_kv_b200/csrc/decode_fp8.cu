@@ -189,6 +189,13 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t v) {
     return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)v, __NV_E4M3)));
 }
 
+// Keeps the uses of loaded TMEM columns below the wait before it.
+template <int N>
+__device__ __forceinline__ void tie(float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+
 // Two fp32 values as a pair of halves.
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
     uint32_t r;
@@ -673,6 +680,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                             tmem_ld_cols<N>(s_at + i0, hi);
                             tmem_ld_cols<N>(s_at + kHP + i0, low);
                             tmem_wait_ld();
+                            tie(r), tie(hi), tie(low);
 #pragma unroll
                             for (int i = 0; i < N; ++i) z[i0 + i] = fmaf(hi[i] + low[i], k * tau[i], fmaf(r[i], a.scale_log2, ls));
                         }
@@ -788,6 +796,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                                     float o[HG];
                                     tmem_ld_cols<HG>(at, o);
                                     tmem_wait_ld();
+                                    tie(o);
 #pragma unroll
                                     for (int i = 0; i < HG; ++i) o[i] *= misc.factor[sg][i];
                                     tmem_st_cols<HG>(at, o);
@@ -868,6 +877,7 @@ decode_fp8_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Dec
                         tmem_ld_cols<N>(at + kHP + i0, o1);
                         tmem_ld_cols<N>(at + 2 * kHP + i0, o2);
                         tmem_wait_ld();
+                        tie(o), tie(o1), tie(o2);
                         if (!mine) continue;
 #pragma unroll
                         for (int i = 0; i < N; ++i) o[i] = bad ? 0.f : fmaf(o2[i], 1.f / 32, fmaf(o1[i], 0.25f, o[i])) * misc.factor[sg][i0 + i];

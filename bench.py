@@ -62,8 +62,8 @@ FALLBACK_HBM_GBS = 6650.0
 # ncu capture (dram__bytes_read.sum + dram__bytes_write.sum), keyed by the
 # hash of the kernel sources it was taken on.  Reported as null whenever the
 # kernel sources differ from the captured ones.
-TRAFFIC_CAPTURE = {"workload": "decode_2p9b", "sources_sha1": "655e97fac1e40fbb51a0ac24b8b96a794f3a45c5",
-                   "bytes_per_launch": 151399680 + 2785536}
+TRAFFIC_CAPTURE = {"workload": "decode_2p9b", "sources_sha1": "4e017be6dc298b491fe940dd2b65f37f1ff9c668",
+                   "bytes_per_launch": 151393280 + 3541248}
 KERNEL_SOURCES = ["branch_latent_kv_b200/csrc/decode_tc.cu", "branch_latent_kv_b200/csrc/sm100.cuh",
                   "branch_latent_kv_b200/csrc/common.cuh", "branch_latent_kv_b200/csrc/decode_split.cuh"]
 

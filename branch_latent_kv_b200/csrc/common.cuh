@@ -175,7 +175,9 @@ __device__ inline void warp_find_seq(const int32_t* seqlens, int batch, int P, i
     *cum_out = base_cum;
 }
 
-// The plan's cost positions are int32: the largest possible total must fit.
+// The plan's cost positions are int32: the largest possible total must fit.  (A
+// larger charge than kSeqCost, up to 20, adds less than 2^21 in kMaxBatch
+// sequences: the sums stay below 2^31 with room for a chunk.)
 inline bool plan_fits_int32(long long batch, long long page_size, long long max_pages) {
     const long long tiles_per_seq = (max_pages * page_size + kTileTokens - 1) / kTileTokens;
     return batch * (tiles_per_seq * kTileCost + kSeqCost) <= (1LL << 30);

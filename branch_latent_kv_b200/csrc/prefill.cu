@@ -533,7 +533,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
         };
         Ring c_new, k_new, c_old;  // the tile of the next scores (latents, keys); the tile of the next PV
         auto landed = [&]() { return mbar_wait_warp(&misc.k_full[k_new.at], k_new.phase) && mbar_wait_warp(&misc.c_full[c_new.at], c_new.phase); };
-        auto scores = [&](int m, int slot, bool last) {  // the elected thread: S[slot] = Q C^T + Qr Kr^T of the new tile
+        auto scores = [&](int m, int slot) {  // the elected thread: S[slot] = Q C^T + Qr Kr^T of the new tile
             const uint32_t d = tmem + slot * C::S_COLS;
             const uint64_t qr = dQr + ((m * C::Q_TILE) >> 4), k0 = dK + ((k_new.at * C::K_BYTES) >> 4);
             const uint64_t q = dQ + ((m * C::Q_TILE) >> 4), c = dC + ((c_new.at * C::C_BYTES) >> 4);
@@ -576,7 +576,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                 if (s == 0 || C::MT == 1) ok = ok && landed();
                 if (ok) {
                     tc_fence_after();
-                    if (elect_one()) scores(C::MT == 2 ? s : 0, slot, (C::MT == 2 ? 1 : s + 1) == ntiles);
+                    if (elect_one()) scores(C::MT == 2 ? s : 0, slot);
                     __syncwarp();
                     if (s == C::MT - 1 || C::MT == 1) c_new.next(C::NC), k_new.next(C::NK);
                 }
@@ -596,7 +596,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                     tc_fence_after();
                     if (elect_one()) {
                         values(m, slot, i == 0, i == ntiles - 1);
-                        if (more) scores(m, slot, i + AHEAD == ntiles - 1);
+                        if (more) scores(m, slot);
                     }
                     __syncwarp();
                 }
@@ -899,9 +899,9 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                 const float4* here = reinterpret_cast<const float4*>(sm + C::OFF_X + slot * C::X_BYTES) + r;
                 ok = mbar_wait_warp(&misc.x_full[slot], parity);
                 if (!ok) {
-                at = end;
-                continue;
-            }
+                    at = end;
+                    continue;
+                }
 #pragma unroll
                 for (int c = 0; c < C::KT / 4; ++c) {
                     const float4 v = here[c * 128];
@@ -915,9 +915,9 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                 // (P will lie over the scores: they have been taken for sending)
                 ok = mbar_wait_warp(&misc.x_taken[slot], parity);
                 if (!ok) {
-                at = end;
-                continue;
-            }
+                    at = end;
+                    continue;
+                }
                 tc_fence_after();
             }
             // tokens j > limit of the tile are masked (a whole warp's rows at once see it all otherwise)
@@ -955,9 +955,9 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
                     if constexpr (C::MT == 1) {
                         ok = mbar_wait_warp(&misc.o_done[(at - 1) & 1], ((at - 1) >> 1) & 1);
                         if (!ok) {
-                at = end;
-                continue;
-            }
+                            at = end;
+                            continue;
+                        }
                         tc_fence_after();
                     }
                     const float alpha = grow ? ex2(mx - top[0]) : 1.f;

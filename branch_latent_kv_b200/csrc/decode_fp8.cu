@@ -24,9 +24,9 @@
 //    what is left (the upper byte of a half is an e5m2 value), the last one
 //    rounded: 9 significant bits, 2^-9 of it.  e5m2 because its exponent is
 //    fp16's; the second and third part are scaled up by 2^2 and 2^5 (their
-//    columns are summed apart), so that nothing above 2^-22 is lost: with the
-//    largest weight at 2^2 .. 2^15 that is 2^-24 of it, in long ranges, whose flat
-//    tails are made of such weights, down to 2^-29.
+//    columns are summed apart), so that nothing above 2^-22 is lost.  The largest
+//    weight lies at 2^2 .. 2^15; in long ranges, whose flat tails are made of small
+//    ones, it is kept higher.
 // The value scales go into the probabilities:
 //   z_t = log2(e) scale s_t + log2 sigma_t,  w_t = 2^(z_t - M) = p_t sigma_t,
 //   o = sum w_t e_t / l,  l = sum w_t / sigma_t,
@@ -51,8 +51,8 @@
 // of four branches, 84.6 MB: 32.6 us back to back (2.6 TB/s): 6.2 us to the
 // first references (lengths, plan, table, queries, first tile), then 2.05 us
 // per tile of each SM (5.4 TB/s), 4 us for the epilogue and 4 for the merge.
-// Longer batches keep more of the rate: 373 MB of ragged lengths 93 us (4.0 TB/s),
-// 337 MB of one 512-wide branch 71 us (4.7 TB/s); tensor pipe at 8 and 14 %.
+// Longer batches keep more of the rate: 373 MB of ragged lengths 92 us (4.1 TB/s),
+// 337 MB of one 512-wide branch 72 us (4.7 TB/s); tensor pipe at 8 and 14 %.
 #include <cuda_fp8.h>
 
 #include <cstddef>
@@ -74,11 +74,12 @@ constexpr int kMaxSteps = 5;
 // The reference M sits 2^base below the largest weight when it is set, and is
 // raised when a weight passes 2^kTop (e5m2 holds 1.75 2^15).  What is left of a
 // weight ends at 2^-22, so a range of n tokens leaves out n 2^-(22 + base) of its
-// largest weight at most: base is log2 n - 11, from 2 (n = 2^13) to kBaseMost.  It is no higher than that asks for, since raises cost: 16 x 8192
-// tokens 32.7 us with 2, 33.9 with 5, 34.6 with 8, the ragged batch 94.9, 96.6,
-// 99.5.  With 2 throughout, 2^18 tokens 2^24.5 below one of no value came out as
-// zero.  (kBaseMost is no 8: where fp32's step is 16, a largest score less 8 can
-// round to 16 below it, a weight of 2^16.)
+// largest weight at most: base is log2 n - 11, from 2 (n = 2^13) to kBaseMost.
+// It is no higher than that asks for, since raises cost: 16 x 8192 tokens 32.7 us
+// with 2, 33.9 with 5, 34.6 with 8, the ragged batch 94.9, 96.6, 99.5.  With 2
+// throughout, 2^18 tokens 2^24.5 below one of no value came out as zero.
+// (kBaseMost is no 8: where fp32's step is 16, a largest score less 8 can round to
+// 16 below it, a weight of 2^16.)
 constexpr float kTop = 15.0f;
 constexpr int kBaseMost = 7;
 // Contexts of up to this many tiles are not split: 64 x 500 tokens of four
@@ -97,9 +98,15 @@ struct Cfg {
     static constexpr int SBR = BPC;                              // branches per step (a chunk is not divided)
     // a range change in cost units of the split plan (a tile is 8): new queries,
     // the first tile's references and an epilogue take about two tiles' time.
-    // 16 x 8192 tokens of four branches: 34.3 us at 4, 33.8 at 12, 32.7 at 20; the
-    // ragged batch 98.8, 98.4, 93.0; one 512-wide branch (a quarter of the
-    // softmax) 72.2 at 4, 71.1 at 12, 73.3 at 20.
+    // us at 4, 12, 20 of 16 x 8192 tokens, 64 ragged sequences and 32 x 16384 tokens:
+    //   4 x 128  33.3 33.1 32.8   96.8 94.6 92.0   85.8 84.0 85.8
+    //   4 x 64   30.2 29.6 28.1   73.9 71.9 71.2   66.5 65.3 65.3
+    //   2 x 256  29.7 30.0 29.8   86.7 85.8 85.6   77.0 76.4 78.3
+    //   2 x 128  23.1 23.4 23.0   60.1 59.9 59.3   54.2 53.0 54.9
+    //   2 x 64   22.0 22.4 22.3   52.0 51.4 49.8   47.6 45.8 45.8
+    //   1 x 512  28.4 28.5 28.8   82.7 82.1 81.4   73.0 72.0 73.9
+    //   1 x 256  21.7 21.8 22.1   57.0 56.6 56.6   50.8 50.2 51.6
+    //   1 x 128  18.5 19.0 18.4   45.4 45.3 45.4   41.4 40.1 41.3
     static constexpr int RANGE_COST = NB == 1 ? 12 : 20;
     static constexpr int HG = kHP * NB / kGroups;                // heads of a softmax group: 16, 8 or 4
     static constexpr int GPB = kGroups / NB;                     // groups per branch

@@ -60,8 +60,10 @@
 //  - d_c = 128, 8192 tokens of 16 heads and four branches: 1.09 PFLOP/s in short
 //    runs (1073 us), 0.93 under the power cap.  An item's softmax (128 scores a
 //    thread, their exponentials on the special-function units) takes 1900 to
-//    2600 cycles, its MMAs 1280 and a pair of items 4550: the two warpgroups
-//    of a scheduler share its issue slots.
+//    2600 cycles, its MMAs 1280 and a pair of items 4550: each row tile is a
+//    chain, its softmax, its output product, its next scores, of which only the
+//    other tile's fills the gaps.  No unit is full: tensor pipe 59 % of the cycles,
+//    special functions 48, issue slots 34.
 //  - d_c = 512: 2900 cycles per 64 tokens, of which the products are 1500: the
 //    exchange of the partial scores is a chain of TMEM read, store, add.
 //  - short prompts: 6 us of dependent reads before an SM's first product, its

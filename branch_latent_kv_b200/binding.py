@@ -129,6 +129,22 @@ def _ptr(t: torch.Tensor) -> int:
     return int(t.data_ptr())
 
 
+def _output(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
+    """The call's output, when the caller gives none.  On a stream of the
+    caller's the memory is that stream's, so that nothing still queued on the
+    current one uses it, and is not given away before the current stream is
+    done with it either."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if stream.cuda_stream == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(current)
+    return out
+
+
 def _require(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int, device: torch.device):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -213,7 +229,7 @@ def _decode_call(call, name, q_lat, q_rope, latent_cache, rope_cache, block_tabl
         raise ValueError("inconsistent mlra_decode shapes")
     dims = decode_dims(q_lat, q_rope, latent_cache, block_table)
     if out is None:
-        out = torch.empty_like(q_lat)
+        out = _output(q_lat.shape, torch.bfloat16, dev, stream)
     else:
         _require(out, "out", torch.bfloat16, 4, dev)
         if out.shape != q_lat.shape:
@@ -259,7 +275,7 @@ def mlra_decode_up_proj(q_lat, q_rope, latent_cache, rope_cache, block_table, se
     if w_uv.shape[2] != H * d_h:
         raise ValueError("w_uv last dimension must be heads*d_h")
     if y is None:
-        y = torch.empty((N, H * d_h), dtype=torch.bfloat16, device=dev)
+        y = _output((N, H * d_h), torch.bfloat16, dev, stream)
     else:
         _require(y, "y", torch.bfloat16, 2, y.device if y.device.type == "cpu" else dev)
         if y.device.type == "cpu" and not y.is_pinned():
@@ -310,7 +326,7 @@ def _up_proj(out_lat, w_uv, gate, d_h, y, stream) -> torch.Tensor:
     if w_uv.shape[2] != H * d_h:
         raise ValueError("w_uv last dimension must be heads*d_h")
     if y is None:
-        y = torch.empty((N, H * d_h), dtype=torch.bfloat16, device=dev)
+        y = _output((N, H * d_h), torch.bfloat16, dev, stream)
     else:
         # y may be pinned host memory: the kernel then writes it over PCIe
         _require(y, "y", torch.bfloat16, 2, y.device if y.device.type == "cpu" else dev)
@@ -363,7 +379,7 @@ def mlra_decode_plan(seqlens: torch.Tensor, page_size: int, max_pages_per_seq: i
     """The split-KV work partition as int32 [num_ctas*4 + N*2] (see mlra.h)."""
     dev = seqlens.device
     _require(seqlens, "seqlens", torch.int32, 1, dev)
-    out = torch.empty(num_ctas * 4 + seqlens.numel() * 2, dtype=torch.int32, device=dev)
+    out = _output((num_ctas * 4 + seqlens.numel() * 2,), torch.int32, dev, stream)
     st = library().mlra_decode_plan(seqlens.numel(), page_size, max_pages_per_seq, _ptr(seqlens),
                                     num_ctas, _ptr(out), _stream_ptr(stream, dev))
     _check(st, "mlra_decode_plan")
@@ -405,11 +421,11 @@ def mlra_prepare(q_c, q_r, w_uk, c_new, kr_new, seqlens, block_table, latent_cac
             or seqlens.shape[0] != N or block_table.shape[0] != N):
         raise ValueError("inconsistent mlra_prepare shapes")
     if q_lat is None:
-        q_lat = torch.empty((N, H, B, d_c), dtype=torch.bfloat16, device=dev)
+        q_lat = _output((N, H, B, d_c), torch.bfloat16, dev, stream)
     else:
         _require(q_lat, "q_lat", torch.bfloat16, 4, dev)
     if q_rope is None:
-        q_rope = torch.empty((N, H, d_r), dtype=torch.bfloat16, device=dev)
+        q_rope = _output((N, H, d_r), torch.bfloat16, dev, stream)
     else:
         _require(q_rope, "q_rope", torch.bfloat16, 3, dev)
     if device_status is not None:
@@ -573,7 +589,7 @@ def mlra_up_proj_allreduce(out_lat, w_uv, regions: torch.Tensor, rank: int, gate
         raise ValueError("w_uv last dimension must be heads*d_h")
     y_shape = ((k,) if lead else ()) + (N, H * d_h)
     if y is None:
-        y = torch.empty(y_shape, dtype=torch.bfloat16, device=dev)
+        y = _output(y_shape, torch.bfloat16, dev, stream)
     else:
         _require(y, "y", torch.bfloat16, 2 + lead, dev)
         if tuple(y.shape) != y_shape:

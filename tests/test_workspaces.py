@@ -97,3 +97,32 @@ def test_errors_of_other_streams_are_found():
         graph.replay()
         assert b.mlra_read_device_error() == b.MLRA_ERR_DEVICE_BAD_SEQLEN
         assert b.mlra_read_device_error() == b.MLRA_OK
+
+
+@pytest.mark.gpu
+def test_an_output_made_for_another_stream_is_not_the_current_ones_memory():
+    """A call on a stream of the caller's must not write memory that was given
+    back on the current stream, where work that uses it may still be queued."""
+    N, H, B, d_c, d_r, d_h = 3, 16, 4, 128, 64, 128
+    g16, _ = _case(55, [300, 20, 4])
+    w_uv = torch.randn(B, d_c, H * d_h, device="cuda").to(torch.bfloat16)
+    w_uk = torch.randn(B, H, d_h, d_c, device="cuda").to(torch.bfloat16)
+    new = [torch.randn(*s, device="cuda").to(torch.bfloat16) for s in ((N, H, d_h), (N, H, d_r), (N, B, d_c), (N, d_r))]
+    out = b.mlra_decode(**g16)
+    y = b.mlra_up_proj(out, w_uv)
+    side = torch.cuda.Stream()
+    for call, shapes in (
+            (lambda: b.mlra_decode(**g16, stream=side), [out.shape]),
+            (lambda: b.mlra_decode_up_proj(**g16, w_uv=w_uv, stream=side), [out.shape, y.shape]),
+            (lambda: b.mlra_up_proj(out, w_uv, stream=side), [y.shape]),
+            (lambda: b.mlra_prepare(new[0], new[1], w_uk, new[2], new[3], g16["seqlens"], g16["block_table"], g16["latent_cache"],
+                                    g16["rope_cache"], stream=side), [out.shape, (N, H, d_r)])):
+        torch.cuda.synchronize()
+        freed = [torch.empty(s, dtype=torch.bfloat16, device="cuda") for s in shapes]
+        held = {t.data_ptr() for t in freed}
+        del freed
+        got = call()
+        side.synchronize()
+        got = got if isinstance(got, tuple) else (got,)
+        assert [tuple(t.shape) for t in got] == [tuple(s) for s in shapes]
+        assert not held & {t.data_ptr() for t in got}

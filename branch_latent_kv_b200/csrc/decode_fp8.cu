@@ -122,7 +122,7 @@ struct Cfg {
     static constexpr int P_PART_BYTES = kT * kHP;                // one part of one branch
     static constexpr int P_BRANCH_BYTES = 3 * P_PART_BYTES;
     static constexpr int P_BYTES = SBR * P_BRANCH_BYTES;
-    static constexpr int MISC_BYTES = 3072;
+    static constexpr int MISC_BYTES = 2560;
     // steps between their score MMA and their output MMA (a tile's and one
     // more); RoPE tiles in flight (more where a tile is a chunk or two); RoPE
     // score slots (one is written again when the steps that read it are over)

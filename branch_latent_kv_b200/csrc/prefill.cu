@@ -990,7 +990,15 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Prefil
             // (a row that has seen no token yet: its scores are all -infinity, and so their
             // differences stay)
             const float ref = mx == -INFINITY ? 0.f : mx;
-            const uint64_t sc2 = pack2(sc, sc), mx2 = pack2(-ref, -ref);
+            // The maximum is a rounded product, the difference below takes it exactly: off by
+            // half a step, which from 2^31 on is 2^7 and more, a weight of infinity or none.
+            // From 2^30 on scores are scaled by the power of two that brings the largest below
+            // 2^31: their steps are 2^6 and more still, so all but the largest weigh nothing.
+            // (8192 tokens 1068 us against 1065 without; other forms, with a vote and the
+            // differences taken beforehand, 1077 to 1124; 512-wide branch 235 us against 232.)
+            const float s = __uint_as_float(min(127u << 23, ((127u + 157u) << 23) - (__float_as_uint(ref) & 0x7f800000u)));
+            const float fac = sc * s, neg = -ref * s;
+            const uint64_t sc2 = pack2(fac, fac), mx2 = pack2(neg, neg);
             uint64_t sum[2] = {0, 0};
 #pragma unroll
             for (int j = 0; j < C::KT; j += 2) {

@@ -118,3 +118,29 @@ def test_prompts_drafts_and_steps_of_a_served_batch():
         o, tol = ref.attend(q, qr, ref.rows(values, table, n, L), ref.rows(pool8[2].cpu(), table, n, L), scale, out_scale, L - 1,
                             2.0 ** -9 + 2.0 ** -11, float(q.abs().max()) * 2.0 ** -10 / 224, ref.rows(sigma, table, n, L))
         ref.within(small[n:n + 1], o, tol, f"mlra_decode_fp8, sequence {n}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("log2", [18, 23, 26, 30, 32, 35, 60])
+@pytest.mark.parametrize("branches,d_c,new,past", [(4, 128, 150, 30), (2, 256, 150, 30), (1, 512, 150, 30), (2, 128, 3, 5000)])
+def test_scores_so_large_that_fp32_steps_by_more_than_one(branches, d_c, new, past, log2):
+    """Every token of a row scores the same, about 2^log2: each row is the mean
+    of the latents it sees, whatever the maximum is rounded to."""
+    H, P, d_r = 16, 64, 64
+    c = _case(74, H, branches, d_c, d_r, P, [new], [past], poison=False)
+    c["q_lat"] = torch.zeros_like(c["q_lat"])
+    c["q_rope"] = torch.zeros_like(c["q_rope"])
+    c["q_rope"][..., 0] = (2.0 ** log2 * (1.0 + torch.arange(new * H) % 128 / 128.0)).view(new, H).to(torch.bfloat16)
+    c["rope_cache"] = torch.zeros_like(c["rope_cache"])
+    c["rope_cache"][..., 0] = 1.0
+    for scale in (0.1, -0.3):
+        c["scale"] = scale
+        status = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+        got = b.mlra_prefill(**_gpu(c), device_status=status)
+        assert int(status.item()) == 0
+        lat = ref.rows(c["latent_cache"], c["block_table"], 0, new + past).double()
+        seen = torch.arange(past + 1, past + new + 1).double()[:, None, None]
+        mean, size = (x.cumsum(0)[past:] / seen * c["out_scale"] for x in (lat, lat.abs()))
+        # equal weights: their rounding to bf16 is one factor, 2^-8 at most
+        tol = 2.0 ** -8 * mean.abs() + size * (2.0 ** -8 + 2.0 ** -17)
+        ref.within(got, mean[:, None].expand(got.shape), tol[:, None].expand(got.shape), f"scale {scale}")
